@@ -12,7 +12,14 @@ The calls, with the names of the C entry points:
 * ``jamba_ssm_x_proj``        -- the projection of the scan's input to dt_low, B
   and C with their RMSNorms (libjamba_ssm_proj.so);
 * ``jamba_ssm_dt_proj``       -- the low-rank product that produces the scan's
-  raw Delta from dt_low (libjamba_ssm_proj.so).
+  raw Delta from dt_low (libjamba_ssm_proj.so);
+* ``jamba_ssm_gated_scan``, ``jamba_ssm_gated_scan_bwd``,
+  ``jamba_ssm_gated_state_update`` -- the gated linear recurrence: whole
+  sequences, their gradients, one token (libjamba_ssm_gated.so);
+* ``jamba_ssm_i8_quant``, ``jamba_ssm_i8_proj`` -- 8-bit projections with a
+  scale for each token and output channel (libjamba_ssm_serve.so);
+* ``jamba_ssm_batch_maps``    -- the maps of a continuous batch from its
+  requests' lengths (libjamba_ssm_serve.so).
 
 Every step of the computation runs in the CUDA kernels of the libraries; this
 module only checks tensor metadata, allocates outputs with PyTorch when the
@@ -26,11 +33,20 @@ import torch
 
 from . import _lib
 from ._lib import JambaSSMError
+from .gated import (jamba_ssm_gated_get_status, jamba_ssm_gated_scan, jamba_ssm_gated_scan_bwd,
+                    jamba_ssm_gated_scan_bwd_workspace_size, jamba_ssm_gated_scan_ckpt,
+                    jamba_ssm_gated_scan_ckpt_size, jamba_ssm_gated_state_update)
+from .serve import (jamba_ssm_batch_maps, jamba_ssm_i8_proj, jamba_ssm_i8_quant,
+                    jamba_ssm_serve_get_status)
 
 __all__ = ["jamba_ssm_scan", "jamba_ssm_state_update", "jamba_ssm_get_status", "scan_plan",
            "jamba_ssm_scan_workspace_size", "jamba_ssm_scan_ckpt_size", "jamba_ssm_scan_bwd",
            "jamba_ssm_scan_bwd_workspace_size", "jamba_ssm_ssd_scan",
            "jamba_ssm_x_proj", "jamba_ssm_dt_proj", "jamba_ssm_proj_get_status",
+           "jamba_ssm_gated_scan", "jamba_ssm_gated_scan_ckpt", "jamba_ssm_gated_scan_ckpt_size",
+           "jamba_ssm_gated_scan_bwd", "jamba_ssm_gated_scan_bwd_workspace_size",
+           "jamba_ssm_gated_state_update", "jamba_ssm_gated_get_status", "jamba_ssm_i8_quant",
+           "jamba_ssm_i8_proj", "jamba_ssm_batch_maps", "jamba_ssm_serve_get_status",
            "JambaSSMError"]
 
 _IO = {torch.bfloat16: _lib.BF16, torch.float32: _lib.F32}

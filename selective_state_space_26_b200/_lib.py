@@ -1,5 +1,5 @@
-"""ctypes view of the C ABIs in include/jamba_ssm.h and include/jamba_ssm_proj.h
-(argument marshalling only).
+"""ctypes view of the C ABIs in include/jamba_ssm.h, jamba_ssm_proj.h,
+jamba_ssm_gated.h and jamba_ssm_serve.h (argument marshalling only).
 
 The structures below mirror the headers field by field.  Loading fails loudly
 when a library has not been built: there is no fallback path.
@@ -13,6 +13,8 @@ import threading
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libjamba_ssm.so")
 PROJ_LIB_PATH = os.path.join(_PKG, "libjamba_ssm_proj.so")
+GATED_LIB_PATH = os.path.join(_PKG, "libjamba_ssm_gated.so")
+SERVE_LIB_PATH = os.path.join(_PKG, "libjamba_ssm_serve.so")
 
 (OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_MISALIGNED, ERR_WORKSPACE, ERR_CUDA, ERR_TIMEOUT,
  ERR_NO_DEVICE) = range(8)
@@ -44,6 +46,28 @@ PROJ_EXPORTS = (
     "jamba_ssm_proj_last_cuda_error",
     "jamba_ssm_proj_abi_version",
 )
+# Every symbol jamba_ssm_gated.h declares.
+GATED_EXPORTS = (
+    "jamba_ssm_gated_scan",
+    "jamba_ssm_gated_scan_ckpt_size",
+    "jamba_ssm_gated_scan_bwd",
+    "jamba_ssm_gated_scan_bwd_workspace_size",
+    "jamba_ssm_gated_state_update",
+    "jamba_ssm_gated_get_status",
+    "jamba_ssm_gated_last_cuda_error",
+    "jamba_ssm_gated_abi_version",
+)
+GATED_CKPT_STEPS = 64  # JAMBA_SSM_GATED_CKPT_STEPS
+# Every symbol jamba_ssm_serve.h declares.
+SERVE_EXPORTS = (
+    "jamba_ssm_i8_quant",
+    "jamba_ssm_i8_proj",
+    "jamba_ssm_batch_maps",
+    "jamba_ssm_serve_get_status",
+    "jamba_ssm_serve_last_cuda_error",
+    "jamba_ssm_serve_abi_version",
+)
+I8_MAX_K = 131056  # JAMBA_SSM_I8_MAX_K
 
 _vp = ctypes.c_void_p
 _fp = ctypes.c_void_p  # float* passed as raw address
@@ -147,6 +171,64 @@ class XProjParams(ctypes.Structure):
     ]
 
 
+def _fields(**kinds):
+    """Fields of one ctypes kind each, in order: name=kind."""
+    return list(kinds.items())
+
+
+class GatedScanParams(ctypes.Structure):
+    _fields_ = _fields(
+        struct_size=ctypes.c_size_t, batch=ctypes.c_int64, seqlen=ctypes.c_int64,
+        d_inner=ctypes.c_int64, io_dtype=ctypes.c_int32, reserved=ctypes.c_int32, x=_vp, g=_vp,
+        z=_vp, x_stride=ctypes.c_int64, g_stride=ctypes.c_int64, z_stride=ctypes.c_int64,
+        rate=_fp, bias=_fp, h0=_fp, out=_vp, h_final=_fp, cu_seqlens=_vp,
+        total_tokens=ctypes.c_int64, state_indices=_vp, initial_indices=_vp,
+        num_slots=ctypes.c_int64, ckpt=_fp, workspace=_vp, workspace_bytes=ctypes.c_size_t)
+
+
+class GatedScanBwdParams(ctypes.Structure):
+    _fields_ = _fields(
+        struct_size=ctypes.c_size_t, batch=ctypes.c_int64, seqlen=ctypes.c_int64,
+        d_inner=ctypes.c_int64, io_dtype=ctypes.c_int32, reserved=ctypes.c_int32, x=_vp, g=_vp,
+        z=_vp, x_stride=ctypes.c_int64, g_stride=ctypes.c_int64, z_stride=ctypes.c_int64,
+        rate=_fp, bias=_fp, h0=_fp, dout=_vp, dh_final=_fp, dx=_vp, dg=_vp, dz=_vp, drate=_fp,
+        dbias=_fp, dh0=_fp, cu_seqlens=_vp, total_tokens=ctypes.c_int64, ckpt=_fp,
+        workspace=_vp, workspace_bytes=ctypes.c_size_t)
+
+
+class GatedStateUpdateParams(ctypes.Structure):
+    _fields_ = _fields(
+        struct_size=ctypes.c_size_t, batch=ctypes.c_int64, d_inner=ctypes.c_int64,
+        io_dtype=ctypes.c_int32, reserved=ctypes.c_int32, state=_fp, x=_vp, g=_vp, z=_vp,
+        x_stride=ctypes.c_int64, g_stride=ctypes.c_int64, z_stride=ctypes.c_int64, rate=_fp,
+        bias=_fp, out=_vp, state_indices=_vp, num_slots=ctypes.c_int64, workspace=_vp,
+        workspace_bytes=ctypes.c_size_t)
+
+
+class I8QuantParams(ctypes.Structure):
+    _fields_ = _fields(
+        struct_size=ctypes.c_size_t, rows=ctypes.c_int64, k=ctypes.c_int64,
+        x_dtype=ctypes.c_int32, reserved=ctypes.c_int32, x=_vp, x_stride=ctypes.c_int64, q=_vp,
+        scale=_fp)
+
+
+class I8ProjParams(ctypes.Structure):
+    _fields_ = _fields(
+        struct_size=ctypes.c_size_t, ntok=ctypes.c_int64, k=ctypes.c_int64, n_out=ctypes.c_int64,
+        out_dtype=ctypes.c_int32, reserved=ctypes.c_int32, q=_vp, q_scale=_fp, w=_vp,
+        w_scale=_fp, bias=_fp, out=_vp, timeout_cycles=ctypes.c_uint64)
+
+
+class BatchMapsParams(ctypes.Structure):
+    _fields_ = _fields(
+        struct_size=ctypes.c_size_t, requests=ctypes.c_int64, max_tokens=ctypes.c_int64,
+        max_blocks=ctypes.c_int64, block_size=ctypes.c_int64, new_lens=_vp, ctx_lens=_vp,
+        free_blocks=_vp, num_free_blocks=ctypes.c_int64, free_slots=_vp,
+        num_free_slots=ctypes.c_int64, block_tables=_vp, request_slots=_vp, cu_seqlens=_vp,
+        positions=_vp, token_request=_vp, slot_map=_vp, state_indices=_vp, initial_indices=_vp,
+        counts=_vp)
+
+
 class JambaSSMError(RuntimeError):
     def __init__(self, status: int, what: str, cuda_error=None):
         self.status = status
@@ -160,6 +242,8 @@ class JambaSSMError(RuntimeError):
 _lock = threading.Lock()
 _lib = None
 _proj_lib = None
+_gated_lib = None
+_serve_lib = None
 
 
 def lib():
@@ -230,6 +314,58 @@ def proj_lib():
                 L.jamba_ssm_proj_abi_version.argtypes = []
                 _proj_lib = L
     return _proj_lib
+
+
+def _load(path: str):
+    if not os.path.exists(path):
+        raise RuntimeError(f"{path} is not built; run selective_state_space_26_b200.build.build()"
+                           " (nvcc, sm_100a). There is no CPU fallback.")
+    return ctypes.CDLL(path)
+
+
+def gated_lib():
+    """Load libjamba_ssm_gated.so (raises if it is missing: build it first)."""
+    global _gated_lib
+    if _gated_lib is None:
+        with _lock:
+            if _gated_lib is None:
+                L = _load(GATED_LIB_PATH)
+                for name, cls in (("scan", GatedScanParams), ("scan_bwd", GatedScanBwdParams),
+                                  ("state_update", GatedStateUpdateParams)):
+                    f = getattr(L, "jamba_ssm_gated_" + name)
+                    f.restype, f.argtypes = ctypes.c_int, [ctypes.POINTER(cls), _vp]
+                L.jamba_ssm_gated_scan_ckpt_size.restype = ctypes.c_size_t
+                L.jamba_ssm_gated_scan_ckpt_size.argtypes = [ctypes.c_int64] * 3
+                L.jamba_ssm_gated_scan_bwd_workspace_size.restype = ctypes.c_size_t
+                L.jamba_ssm_gated_scan_bwd_workspace_size.argtypes = [ctypes.c_int64] * 3 + [
+                    ctypes.c_int32]
+                L.jamba_ssm_gated_get_status.restype = ctypes.c_int
+                L.jamba_ssm_gated_get_status.argtypes = [_vp, _vp]
+                for name in ("last_cuda_error", "abi_version"):
+                    f = getattr(L, "jamba_ssm_gated_" + name)
+                    f.restype, f.argtypes = ctypes.c_int, []
+                _gated_lib = L
+    return _gated_lib
+
+
+def serve_lib():
+    """Load libjamba_ssm_serve.so (raises if it is missing: build it first)."""
+    global _serve_lib
+    if _serve_lib is None:
+        with _lock:
+            if _serve_lib is None:
+                L = _load(SERVE_LIB_PATH)
+                for name, cls in (("i8_quant", I8QuantParams), ("i8_proj", I8ProjParams),
+                                  ("batch_maps", BatchMapsParams)):
+                    f = getattr(L, "jamba_ssm_" + name)
+                    f.restype, f.argtypes = ctypes.c_int, [ctypes.POINTER(cls), _vp]
+                L.jamba_ssm_serve_get_status.restype = ctypes.c_int
+                L.jamba_ssm_serve_get_status.argtypes = [_vp]
+                for name in ("last_cuda_error", "abi_version"):
+                    f = getattr(L, "jamba_ssm_serve_" + name)
+                    f.restype, f.argtypes = ctypes.c_int, []
+                _serve_lib = L
+    return _serve_lib
 
 
 def status_string(status: int) -> str:

@@ -1,0 +1,91 @@
+"""Checks of tensor arguments and the choice of device and stream, shared by the
+gated recurrence's and the serving step's bindings."""
+from __future__ import annotations
+
+import contextlib
+
+import torch
+
+from . import _lib
+
+IO = {torch.bfloat16: _lib.BF16, torch.float32: _lib.F32}
+_HERE = contextlib.nullcontext()
+
+
+def ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def check(t, name, shape, dtype, device):
+    """A contiguous tensor of this shape, dtype and device (or None)."""
+    if t is None:
+        return
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def row_stride(t, name, shape, dtype, device):
+    """Elements between the rows of an activation whose channels are contiguous
+    and whose rows are evenly spaced (0 for None or a contiguous tensor)."""
+    if t is None:
+        return 0
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.is_contiguous():
+        return 0
+    # the dimensions before the channels, outermost first, those of one row left out
+    dims = [(n, s) for n, s in zip(t.shape[:-1], t.stride()[:-1]) if n != 1]
+    width = t.shape[-1]
+    even = all(dims[i][1] == dims[i + 1][0] * dims[i + 1][1] for i in range(len(dims) - 1))
+    if (width > 1 and t.stride(-1) != 1) or not even or (dims and dims[-1][1] < width):
+        raise ValueError(f"{name} must have contiguous channels and evenly spaced rows "
+                         f"(shape {tuple(t.shape)}, strides {t.stride()})")
+    return dims[-1][1] if dims else 0
+
+
+def cuda_device(t, name, what):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{what} needs CUDA tensors; there is no CPU path")
+    return t.device
+
+
+def launching(stream, device):
+    """Context for a call's allocations and launch: the tensors' device is the
+    current one and, where the caller names a stream, that stream too, so what
+    is allocated for the call belongs to the stream that uses it."""
+    if stream is None:
+        return _HERE if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+    if not isinstance(stream, torch.cuda.Stream):
+        raw = int(getattr(stream, "cuda_stream", stream))
+        stream = torch.cuda.ExternalStream(raw, device=device) if raw else \
+            torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
+
+
+def raw_stream(device):
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def workspace(ws, device):
+    """(pointer, bytes) of an optional workspace tensor."""
+    if ws is None:
+        return None, 0
+    if not isinstance(ws, torch.Tensor) or ws.device != device or not ws.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the device of the inputs")
+    return ws.data_ptr(), ws.numel() * ws.element_size()

@@ -1,11 +1,13 @@
 """Build the CUDA libraries in-tree for sm_100a with nvcc: libjamba_ssm.so
-(the scan and the decode update) and libjamba_ssm_proj.so (the projection that
-feeds the scan)."""
+(the scan and the decode update), libjamba_ssm_proj.so (the projection that
+feeds the scan), libjamba_ssm_gated.so (the gated linear recurrence) and
+libjamba_ssm_serve.so (8-bit projections and the maps of a continuous batch)."""
 from __future__ import annotations
 
 import os
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -13,12 +15,17 @@ SRC = os.path.join(PKG, "csrc", "jamba_ssm.cu")
 LIB = os.path.join(PKG, "libjamba_ssm.so")
 PROJ_SRC = os.path.join(PKG, "csrc", "jamba_ssm_proj.cu")
 PROJ_LIB = os.path.join(PKG, "libjamba_ssm_proj.so")
+GATED_SRC = os.path.join(PKG, "csrc", "jamba_ssm_gated.cu")
+GATED_LIB = os.path.join(PKG, "libjamba_ssm_gated.so")
+SERVE_SRC = os.path.join(PKG, "csrc", "jamba_ssm_serve.cu")
+SERVE_LIB = os.path.join(PKG, "libjamba_ssm_serve.so")
+ALL = ((SRC, LIB), (PROJ_SRC, PROJ_LIB), (GATED_SRC, GATED_LIB), (SERVE_SRC, SERVE_LIB))
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 
 def sources():
     d = os.path.join(PKG, "csrc")
-    return [os.path.join(d, f) for f in sorted(os.listdir(d)) if f.endswith((".cu", ".cuh"))]
+    return [os.path.join(d, f) for f in sorted(os.listdir(d)) if f.endswith((".cu", ".cuh", ".h"))]
 
 
 def up_to_date(lib: str = LIB) -> bool:
@@ -36,7 +43,7 @@ def _nvcc(src: str, out: str, verbose: bool) -> None:
     cmd = [NVCC, "-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo",
            "-std=c++17", "-Xcompiler", "-fPIC", "-shared", "-cudart", "static",
            "-I", os.path.join(ROOT, "include"), "-o", out, src]
-    if out == PROJ_LIB:
+    if out != LIB:
         cmd[cmd.index("-fPIC")] = "-fPIC,-fvisibility=hidden"
     if verbose:
         cmd.insert(1, "-Xptxas=-v")
@@ -44,13 +51,13 @@ def _nvcc(src: str, out: str, verbose: bool) -> None:
 
 
 def build(verbose: bool = False, force: bool = False) -> str:
-    for src, out in ((SRC, LIB), (PROJ_SRC, PROJ_LIB)):
-        if force or not up_to_date(out):
-            _nvcc(src, out, verbose)
+    todo = [(src, out) for src, out in ALL if force or not up_to_date(out)]
+    with ThreadPoolExecutor(len(ALL)) as pool:  # one nvcc each
+        list(pool.map(lambda so: _nvcc(so[0], so[1], verbose), todo))
     return LIB
 
 
 if __name__ == "__main__":
     build(verbose="-v" in sys.argv, force=True)
-    print(LIB)
-    print(PROJ_LIB)
+    for _, lib in ALL:
+        print(lib)

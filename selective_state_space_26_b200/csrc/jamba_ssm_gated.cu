@@ -1,0 +1,278 @@
+// jamba_ssm_gated.cu -- host side of the C ABI declared in
+// include/jamba_ssm_gated.h: argument validation and the launches of the gated
+// recurrence's kernels.  Built as its own library, so its kernels and status
+// word form a module of their own.  Nothing here allocates device memory.
+#include "jamba_ssm_gated.h"
+
+#include "gated_scan.cuh"
+#include "host_utils.h"
+
+#define JSSM_GATED_API extern "C" __attribute__((visibility("default")))
+
+using namespace jssm_host;
+
+namespace {
+
+constexpr int64_t kMaxRows = int64_t(1) << 30, kMaxBatch = int64_t(1) << 24,
+                  kMaxWidth = int64_t(1) << 20;
+
+// Bytes from a strided activation's first element to its last one's end.
+size_t span(int64_t rows, int64_t stride, int64_t d, int es) {
+    return rows > 0 ? size_t((rows - 1) * stride + d) * es : 0;
+}
+
+// What the scan and its backward check alike.  Resolves the strides of 0.
+template <typename P> jamba_ssm_status check_common(P *p, int64_t *rows) {
+    if (p->batch < 0 || p->seqlen < 0 || p->d_inner < 1 || p->reserved != 0)
+        return JAMBA_SSM_ERR_INVALID_ARG;
+    if (p->io_dtype != JAMBA_SSM_BF16 && p->io_dtype != JAMBA_SSM_F32) return JAMBA_SSM_ERR_INVALID_ARG;
+    if (p->cu_seqlens && p->total_tokens < 0) return JAMBA_SSM_ERR_INVALID_ARG;
+    for (int64_t *s : {&p->x_stride, &p->g_stride, &p->z_stride}) {
+        if (*s == 0) *s = p->d_inner;
+        if (*s < p->d_inner) return JAMBA_SSM_ERR_INVALID_ARG;
+        if (*s > (int64_t(1) << 31)) return JAMBA_SSM_ERR_UNSUPPORTED;
+    }
+    if (p->batch > kMaxBatch || p->d_inner > kMaxWidth || p->seqlen > kMaxRows)
+        return JAMBA_SSM_ERR_UNSUPPORTED;
+    *rows = p->cu_seqlens ? p->total_tokens : p->batch * p->seqlen;
+    if (*rows > kMaxRows) return JAMBA_SSM_ERR_UNSUPPORTED;
+    if (!aligned(p->cu_seqlens, 4) || !aligned(p->rate, 4) || !aligned(p->bias, 4) ||
+        !aligned(p->h0, 4))
+        return JAMBA_SSM_ERR_MISALIGNED;
+    const int es = p->io_dtype == JAMBA_SSM_BF16 ? 2 : 4;
+    if (!aligned(p->x, es) || !aligned(p->g, es) || !aligned(p->z, es)) return JAMBA_SSM_ERR_MISALIGNED;
+    return JAMBA_SSM_OK;
+}
+
+template <typename P> void fill_common(const P &p, int64_t rows, jssm::GatedArgs *a) {
+    a->x = p.x;
+    a->g = p.g;
+    a->z = p.z;
+    a->xs = p.x_stride;
+    a->gs = p.g_stride;
+    a->zs = p.z_stride;
+    a->rate = p.rate;
+    a->bias = p.bias;
+    a->h0 = p.h0;
+    a->cu = p.cu_seqlens;
+    a->total = rows;
+    a->seqlen = p.seqlen;
+    a->d = static_cast<int>(p.d_inner);
+    a->batch = static_cast<int>(p.batch);
+}
+
+jamba_ssm_status launch(const void *k, unsigned grid, unsigned threads, void **args, void *stream) {
+    cudaError_t e = cudaLaunchKernel(k, dim3(grid), dim3(threads), args, 0,
+                                     static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? JAMBA_SSM_OK : cuda_fail(e);
+}
+
+jamba_ssm_status launch_scan(jssm::GatedArgs &a, int32_t dtype, void *stream) {
+    void *args[] = {&a};
+    const int64_t n = int64_t(a.batch) * a.d;
+    const int64_t grid = (n + 127) / 128;
+    if (grid > 0x7fffffff) return JAMBA_SSM_ERR_UNSUPPORTED;
+    return launch(dtype == JAMBA_SSM_BF16 ? (const void *)&jssm::gated_scan_kernel<__nv_bfloat16>
+                                          : (const void *)&jssm::gated_scan_kernel<float>,
+                  static_cast<unsigned>(grid), 128, args, stream);
+}
+
+size_t ckpt_bytes(int64_t batch, int64_t rows, int64_t d) {
+    return size_t(rows / JAMBA_SSM_GATED_CKPT_STEPS + batch) * size_t(d) * 4;
+}
+size_t partial_bytes(int64_t batch, int64_t d) { return size_t(batch) * 2 * size_t(d) * 4; }
+
+}  // namespace
+
+JSSM_GATED_API size_t jamba_ssm_gated_scan_ckpt_size(int64_t batch, int64_t rows, int64_t d_inner) {
+    return batch < 0 || rows < 0 || d_inner < 0 ? 0 : ckpt_bytes(batch, rows, d_inner);
+}
+
+JSSM_GATED_API size_t jamba_ssm_gated_scan_bwd_workspace_size(int64_t batch, int64_t rows,
+                                                              int64_t d_inner, int32_t has_ckpt) {
+    if (batch < 0 || rows < 0 || d_inner < 0) return 0;
+    return partial_bytes(batch, d_inner) + (has_ckpt ? 0 : ckpt_bytes(batch, rows, d_inner));
+}
+
+JSSM_GATED_API jamba_ssm_status jamba_ssm_gated_scan(const jamba_ssm_gated_scan_params *pin,
+                                                     void *stream) {
+    jamba_ssm_gated_scan_params p;
+    if (!read_params(pin, &p)) return JAMBA_SSM_ERR_INVALID_ARG;
+    int64_t rows = 0;
+    jamba_ssm_status st = check_common(&p, &rows);
+    if (st != JAMBA_SSM_OK) return st;
+    if (p.initial_indices && !p.state_indices) return JAMBA_SSM_ERR_INVALID_ARG;
+    if (p.state_indices && p.num_slots < 1) return JAMBA_SSM_ERR_INVALID_ARG;
+    if (p.num_slots > 0x7fffffff) return JAMBA_SSM_ERR_UNSUPPORTED;
+    const int es = p.io_dtype == JAMBA_SSM_BF16 ? 2 : 4;
+    if (!aligned(p.state_indices, 4) || !aligned(p.initial_indices, 4) || !aligned(p.out, es) ||
+        !aligned(p.h_final, 4) || !aligned(p.ckpt, 16))
+        return JAMBA_SSM_ERR_MISALIGNED;
+    if ((st = check_workspace(p.workspace, p.workspace_bytes)) != JAMBA_SSM_OK) return st;
+    if (p.batch == 0) return JAMBA_SSM_OK;  // no work; the pointers are not used
+    if (rows > 0 && (!p.x || !p.g || !p.out)) return JAMBA_SSM_ERR_INVALID_ARG;
+    const size_t act = size_t(rows) * p.d_inner * es;
+    const size_t state = size_t(p.state_indices ? p.num_slots : p.batch) * p.d_inner * 4;
+    const Range ins[] = {{p.x, span(rows, p.x_stride, p.d_inner, es)},
+                         {p.g, span(rows, p.g_stride, p.d_inner, es)},
+                         {p.z, span(rows, p.z_stride, p.d_inner, es)},
+                         {p.rate, size_t(p.d_inner) * 4},
+                         {p.bias, size_t(p.d_inner) * 4},
+                         {p.cu_seqlens, size_t(p.batch + 1) * 4},
+                         {p.state_indices, size_t(p.batch) * 4},
+                         {p.initial_indices, size_t(p.batch) * 4},
+                         {p.h0 == p.h_final ? nullptr : p.h0, state}};
+    const Range outs[] = {{p.out, act},
+                          {p.h_final, state},
+                          {p.ckpt, ckpt_bytes(p.batch, rows, p.d_inner)},
+                          {p.workspace, size_t(JAMBA_SSM_STATUS_BYTES)}};
+    if (any_overlap(outs, 4, ins, 9)) return JAMBA_SSM_ERR_INVALID_ARG;
+    if (!current_device(&st)) return st;
+
+    jssm::GatedArgs a{};
+    fill_common(p, rows, &a);
+    a.out = p.out;
+    a.h_final = p.h_final;
+    a.state_indices = p.state_indices;
+    a.initial_indices = p.initial_indices;
+    a.num_slots = p.num_slots;
+    a.ckpt = p.ckpt;
+    a.status = static_cast<int *>(p.workspace);
+    if ((st = launch_scan(a, p.io_dtype, stream)) != JAMBA_SSM_OK) return st;
+    return finish_launch(stream, p.workspace);
+}
+
+JSSM_GATED_API jamba_ssm_status
+jamba_ssm_gated_scan_bwd(const jamba_ssm_gated_scan_bwd_params *pin, void *stream) {
+    jamba_ssm_gated_scan_bwd_params p;
+    if (!read_params(pin, &p)) return JAMBA_SSM_ERR_INVALID_ARG;
+    int64_t rows = 0;
+    jamba_ssm_status st = check_common(&p, &rows);
+    if (st != JAMBA_SSM_OK) return st;
+    const int es = p.io_dtype == JAMBA_SSM_BF16 ? 2 : 4;
+    if (!aligned(p.dout, es) || !aligned(p.dx, es) || !aligned(p.dg, es) || !aligned(p.dz, es) ||
+        !aligned(p.dh_final, 4) || !aligned(p.drate, 4) || !aligned(p.dbias, 4) ||
+        !aligned(p.dh0, 4) || !aligned(p.ckpt, 16) || !aligned(p.workspace, 16))
+        return JAMBA_SSM_ERR_MISALIGNED;
+    const size_t need = jamba_ssm_gated_scan_bwd_workspace_size(p.batch, rows, p.d_inner, p.ckpt != nullptr);
+    if (need > 0 && (!p.workspace || p.workspace_bytes < need)) return JAMBA_SSM_ERR_WORKSPACE;
+    if (rows > 0 && p.batch > 0 &&
+        (!p.x || !p.g || !p.dout || !p.dx || !p.dg || (p.z != nullptr) != (p.dz != nullptr)))
+        return JAMBA_SSM_ERR_INVALID_ARG;
+    const size_t act = size_t(rows) * p.d_inner * es, state = size_t(p.batch) * p.d_inner * 4;
+    const size_t par = size_t(p.d_inner) * 4;
+    const Range ins[] = {{p.x, span(rows, p.x_stride, p.d_inner, es)},
+                         {p.g, span(rows, p.g_stride, p.d_inner, es)},
+                         {p.z, span(rows, p.z_stride, p.d_inner, es)},
+                         {p.rate, par},
+                         {p.bias, par},
+                         {p.cu_seqlens, size_t(p.batch + 1) * 4},
+                         {p.h0, state},
+                         {p.dout, act},
+                         {p.dh_final, state},
+                         {p.ckpt, ckpt_bytes(p.batch, rows, p.d_inner)}};
+    const Range outs[] = {{p.dx, act},   {p.dg, act},    {p.dz, act},   {p.drate, par},
+                          {p.dbias, par}, {p.dh0, state}, {p.workspace, need}};
+    if (any_overlap(outs, 7, ins, 10)) return JAMBA_SSM_ERR_INVALID_ARG;
+    if (!current_device(&st)) return st;
+
+    jssm::GatedArgs a{};
+    fill_common(p, rows, &a);
+    a.dout = p.dout;
+    a.dh_final = p.dh_final;
+    a.dx = p.dx;
+    a.dg = p.dg;
+    a.dz = p.dz;
+    a.drate = p.drate;
+    a.dbias = p.dbias;
+    a.dh0 = p.dh0;
+    a.partial = static_cast<float *>(p.workspace);
+    a.ckpt = const_cast<float *>(p.ckpt);
+    void *args[] = {&a};
+    if (p.batch > 0) {
+        if (!a.ckpt) {
+            a.ckpt = a.partial + partial_bytes(p.batch, p.d_inner) / 4;
+            if ((st = launch_scan(a, p.io_dtype, stream)) != JAMBA_SSM_OK) return st;
+        }
+        const int64_t grid = (p.batch * p.d_inner + 127) / 128;
+        if (grid > 0x7fffffff) return JAMBA_SSM_ERR_UNSUPPORTED;
+        st = launch(p.io_dtype == JAMBA_SSM_BF16
+                        ? (const void *)&jssm::gated_scan_bwd_kernel<__nv_bfloat16>
+                        : (const void *)&jssm::gated_scan_bwd_kernel<float>,
+                    static_cast<unsigned>(grid), 128, args, stream);
+        if (st != JAMBA_SSM_OK) return st;
+    }
+    if (a.drate || a.dbias) {
+        void *rargs[] = {&a.partial, &a.drate, &a.dbias, &a.batch, &a.d};
+        st = launch((const void *)&jssm::gated_reduce_kernel, unsigned((a.d + 127) / 128), 128, rargs, stream);
+        if (st != JAMBA_SSM_OK) return st;
+    }
+    return finish_launch(stream, nullptr);
+}
+
+JSSM_GATED_API jamba_ssm_status
+jamba_ssm_gated_state_update(const jamba_ssm_gated_state_update_params *pin, void *stream) {
+    jamba_ssm_gated_state_update_params p;
+    if (!read_params(pin, &p)) return JAMBA_SSM_ERR_INVALID_ARG;
+    if (p.batch < 0 || p.d_inner < 1 || p.reserved != 0) return JAMBA_SSM_ERR_INVALID_ARG;
+    if (p.io_dtype != JAMBA_SSM_BF16 && p.io_dtype != JAMBA_SSM_F32) return JAMBA_SSM_ERR_INVALID_ARG;
+    if (p.state_indices && p.num_slots < 1) return JAMBA_SSM_ERR_INVALID_ARG;
+    for (int64_t *s : {&p.x_stride, &p.g_stride, &p.z_stride}) {
+        if (*s == 0) *s = p.d_inner;
+        if (*s < p.d_inner) return JAMBA_SSM_ERR_INVALID_ARG;
+        if (*s > (int64_t(1) << 31)) return JAMBA_SSM_ERR_UNSUPPORTED;
+    }
+    if (p.batch > kMaxBatch || p.d_inner > kMaxWidth || p.num_slots > 0x7fffffff)
+        return JAMBA_SSM_ERR_UNSUPPORTED;
+    const int es = p.io_dtype == JAMBA_SSM_BF16 ? 2 : 4;
+    if (!aligned(p.x, es) || !aligned(p.g, es) || !aligned(p.z, es) || !aligned(p.out, es) ||
+        !aligned(p.state, 4) || !aligned(p.rate, 4) || !aligned(p.bias, 4) || !aligned(p.state_indices, 4))
+        return JAMBA_SSM_ERR_MISALIGNED;
+    jamba_ssm_status st = check_workspace(p.workspace, p.workspace_bytes);
+    if (st != JAMBA_SSM_OK) return st;
+    if (p.batch == 0) return JAMBA_SSM_OK;
+    if (!p.state || !p.x || !p.g || !p.out) return JAMBA_SSM_ERR_INVALID_ARG;
+    const size_t state = size_t(p.state_indices ? p.num_slots : p.batch) * p.d_inner * 4;
+    const Range ins[] = {{p.x, span(p.batch, p.x_stride, p.d_inner, es)},
+                         {p.g, span(p.batch, p.g_stride, p.d_inner, es)},
+                         {p.z, span(p.batch, p.z_stride, p.d_inner, es)},
+                         {p.rate, size_t(p.d_inner) * 4},
+                         {p.bias, size_t(p.d_inner) * 4},
+                         {p.state_indices, size_t(p.batch) * 4}};
+    const Range outs[] = {{p.out, size_t(p.batch) * p.d_inner * es},
+                          {p.state, state},
+                          {p.workspace, size_t(JAMBA_SSM_STATUS_BYTES)}};
+    if (any_overlap(outs, 3, ins, 6)) return JAMBA_SSM_ERR_INVALID_ARG;
+    if (!current_device(&st)) return st;
+
+    jssm::GatedUpdateArgs a{};
+    a.state = p.state;
+    a.x = p.x;
+    a.g = p.g;
+    a.z = p.z;
+    a.xs = p.x_stride;
+    a.gs = p.g_stride;
+    a.zs = p.z_stride;
+    a.rate = p.rate;
+    a.bias = p.bias;
+    a.out = p.out;
+    a.state_indices = p.state_indices;
+    a.num_slots = p.num_slots;
+    a.status = static_cast<int *>(p.workspace);
+    a.d = static_cast<int>(p.d_inner);
+    a.batch = static_cast<int>(p.batch);
+    void *args[] = {&a};
+    const int64_t grid = (p.batch * p.d_inner + 255) / 256;
+    if (grid > 0x7fffffff) return JAMBA_SSM_ERR_UNSUPPORTED;
+    st = launch(p.io_dtype == JAMBA_SSM_BF16 ? (const void *)&jssm::gated_update_kernel<__nv_bfloat16>
+                                             : (const void *)&jssm::gated_update_kernel<float>,
+                static_cast<unsigned>(grid), 256, args, stream);
+    if (st != JAMBA_SSM_OK) return st;
+    return finish_launch(stream, p.workspace);
+}
+
+JSSM_GATED_API jamba_ssm_status jamba_ssm_gated_get_status(void *workspace, void *stream) {
+    return read_status(workspace, stream);
+}
+JSSM_GATED_API int jamba_ssm_gated_last_cuda_error(void) { return t_last_cuda_error; }
+JSSM_GATED_API int jamba_ssm_gated_abi_version(void) { return JAMBA_SSM_GATED_ABI_VERSION; }

@@ -1,0 +1,183 @@
+// jamba_ssm_serve.cu -- host side of the C ABI declared in
+// include/jamba_ssm_serve.h: argument validation and the launches of the 8-bit
+// product's and the batch maps' kernels.  Built as its own library, so its
+// kernels and status word form a module of their own.  Nothing here allocates
+// device memory.
+#include "jamba_ssm_serve.h"
+
+#include "batch_maps.cuh"
+#include "host_utils.h"
+#include "i8_proj.cuh"
+#include "i8_quant.cuh"
+
+#define JSSM_SERVE_API extern "C" __attribute__((visibility("default")))
+
+using namespace jssm_host;
+
+namespace {
+
+constexpr int64_t kMaxRows = (int64_t(1) << 31) - (int64_t(1) << 16);
+
+jamba_ssm_status launch(const void *k, dim3 grid, dim3 threads, void **args, size_t smem, void *stream) {
+    cudaError_t e = cudaLaunchKernel(k, grid, threads, args, smem, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? JAMBA_SSM_OK : cuda_fail(e);
+}
+
+bool io_dtype(int32_t d) { return d == JAMBA_SSM_BF16 || d == JAMBA_SSM_F32; }
+
+}  // namespace
+
+JSSM_SERVE_API jamba_ssm_status jamba_ssm_i8_quant(const jamba_ssm_i8_quant_params *pin, void *stream) {
+    jamba_ssm_i8_quant_params p;
+    if (!read_params(pin, &p)) return JAMBA_SSM_ERR_INVALID_ARG;
+    if (p.rows < 0 || p.k < 1 || p.reserved != 0 || !io_dtype(p.x_dtype)) return JAMBA_SSM_ERR_INVALID_ARG;
+    if (p.x_stride == 0) p.x_stride = p.k;
+    if (p.x_stride < p.k) return JAMBA_SSM_ERR_INVALID_ARG;
+    if (p.rows > kMaxRows || p.k > JAMBA_SSM_I8_MAX_K || p.x_stride > (int64_t(1) << 31))
+        return JAMBA_SSM_ERR_UNSUPPORTED;
+    if (p.rows == 0) return JAMBA_SSM_OK;  // no work; the pointers are not used
+    if (!p.x || !p.q || !p.scale) return JAMBA_SSM_ERR_INVALID_ARG;
+    const int es = p.x_dtype == JAMBA_SSM_BF16 ? 2 : 4;
+    if (!aligned(p.x, es) || !aligned(p.q, 16) || !aligned(p.scale, 4)) return JAMBA_SSM_ERR_MISALIGNED;
+    const int64_t pitch = JAMBA_SSM_I8_PITCH(p.k);
+    const Range ins[] = {{p.x, size_t((p.rows - 1) * p.x_stride + p.k) * es}};
+    const Range outs[] = {{p.q, size_t(p.rows) * pitch}, {p.scale, size_t(p.rows) * 4}};
+    if (any_overlap(outs, 2, ins, 1)) return JAMBA_SSM_ERR_INVALID_ARG;
+    jamba_ssm_status st;
+    if (!current_device(&st)) return st;
+    jssm::I8QuantArgs a{};
+    a.x = p.x;
+    a.xs = p.x_stride;
+    a.q = p.q;
+    a.scale = p.scale;
+    a.rows = p.rows;
+    a.k = static_cast<int>(p.k);
+    a.pitch = static_cast<int>(pitch);
+    void *args[] = {&a};
+    st = launch(p.x_dtype == JAMBA_SSM_BF16 ? (const void *)&jssm::i8_quant_kernel<__nv_bfloat16>
+                                            : (const void *)&jssm::i8_quant_kernel<float>,
+                dim3(unsigned(p.rows)), dim3(128), args, 0, stream);
+    return st != JAMBA_SSM_OK ? st : finish_launch(stream, nullptr);
+}
+
+JSSM_SERVE_API jamba_ssm_status jamba_ssm_i8_proj(const jamba_ssm_i8_proj_params *pin, void *stream) {
+    jamba_ssm_i8_proj_params p;
+    if (!read_params(pin, &p)) return JAMBA_SSM_ERR_INVALID_ARG;
+    if (p.ntok < 0 || p.k < 1 || p.n_out < 1 || p.reserved != 0 || !io_dtype(p.out_dtype))
+        return JAMBA_SSM_ERR_INVALID_ARG;
+    if (p.ntok > kMaxRows || p.k > JAMBA_SSM_I8_MAX_K || p.n_out > (int64_t(1) << 24))
+        return JAMBA_SSM_ERR_UNSUPPORTED;
+    if (p.ntok == 0) return JAMBA_SSM_OK;  // no work; the pointers are not used
+    if (!p.q || !p.q_scale || !p.w || !p.w_scale || !p.out) return JAMBA_SSM_ERR_INVALID_ARG;
+    const int es = p.out_dtype == JAMBA_SSM_BF16 ? 2 : 4;
+    if (!aligned(p.q, 16) || !aligned(p.w, 16) || !aligned(p.q_scale, 4) || !aligned(p.w_scale, 4) ||
+        !aligned(p.bias, 4) || !aligned(p.out, es))
+        return JAMBA_SSM_ERR_MISALIGNED;
+    const int64_t pitch = JAMBA_SSM_I8_PITCH(p.k);
+    const Range ins[] = {{p.q, size_t(p.ntok) * pitch},
+                         {p.w, size_t(p.n_out) * pitch},
+                         {p.q_scale, size_t(p.ntok) * 4},
+                         {p.w_scale, size_t(p.n_out) * 4},
+                         {p.bias, size_t(p.n_out) * 4}};
+    const Range outs[] = {{p.out, size_t(p.ntok) * p.n_out * es}};
+    if (any_overlap(outs, 1, ins, 5)) return JAMBA_SSM_ERR_INVALID_ARG;
+    jamba_ssm_status st;
+    if (!current_device(&st)) return st;
+    jssm::I8ProjArgs a{};
+    a.q = p.q;
+    a.w = p.w;
+    a.qs = p.q_scale;
+    a.ws = p.w_scale;
+    a.bias = p.bias;
+    a.out = p.out;
+    a.n = static_cast<int>(p.n_out);
+    a.pitch = static_cast<int>(pitch);
+    void *args[] = {&a};
+    // at most 65535 x 8 tokens fit one grid
+    for (int64_t t = 0; t < p.ntok; t += 65535 * 8) {
+        a.ntok = p.ntok - t < 65535 * 8 ? p.ntok - t : 65535 * 8;
+        a.q = p.q + t * pitch;
+        a.qs = p.q_scale + t;
+        a.out = static_cast<char *>(p.out) + size_t(t) * p.n_out * es;
+        st = launch(p.out_dtype == JAMBA_SSM_BF16 ? (const void *)&jssm::i8_proj_simple_kernel<__nv_bfloat16>
+                                                  : (const void *)&jssm::i8_proj_simple_kernel<float>,
+                    dim3(unsigned((p.n_out + 31) / 32), unsigned((a.ntok + 7) / 8)), dim3(32, 8), args, 0,
+                    stream);
+        if (st != JAMBA_SSM_OK) return st;
+    }
+    return finish_launch(stream, nullptr);
+}
+
+JSSM_SERVE_API jamba_ssm_status jamba_ssm_batch_maps(const jamba_ssm_batch_maps_params *pin, void *stream) {
+    jamba_ssm_batch_maps_params p;
+    if (!read_params(pin, &p)) return JAMBA_SSM_ERR_INVALID_ARG;
+    if (p.requests < 0 || p.max_tokens < 0 || p.max_blocks < 1 || p.block_size < 1 ||
+        p.num_free_blocks < 0 || p.num_free_slots < 0)
+        return JAMBA_SSM_ERR_INVALID_ARG;
+    if (p.requests > (int64_t(1) << 20) || p.max_tokens > (int64_t(1) << 30) ||
+        p.max_blocks > (int64_t(1) << 24) || p.block_size > (int64_t(1) << 20) ||
+        p.num_free_blocks > 0x7fffffff || p.num_free_slots > 0x7fffffff)
+        return JAMBA_SSM_ERR_UNSUPPORTED;
+    if (!p.cu_seqlens || !p.counts || (p.num_free_blocks > 0 && !p.free_blocks) ||
+        (p.num_free_slots > 0 && !p.free_slots))
+        return JAMBA_SSM_ERR_INVALID_ARG;
+    if (p.requests > 0 && (!p.new_lens || !p.block_tables || !p.request_slots || !p.state_indices ||
+                           !p.initial_indices))
+        return JAMBA_SSM_ERR_INVALID_ARG;
+    if (p.max_tokens > 0 && (!p.positions || !p.token_request || !p.slot_map))
+        return JAMBA_SSM_ERR_INVALID_ARG;
+    for (const void *q : {(const void *)p.new_lens, (const void *)p.ctx_lens, (const void *)p.free_blocks,
+                          (const void *)p.free_slots, (const void *)p.block_tables,
+                          (const void *)p.request_slots, (const void *)p.cu_seqlens,
+                          (const void *)p.positions, (const void *)p.token_request,
+                          (const void *)p.state_indices, (const void *)p.initial_indices,
+                          (const void *)p.counts})
+        if (!aligned(q, 4)) return JAMBA_SSM_ERR_MISALIGNED;
+    if (!aligned(p.slot_map, 8)) return JAMBA_SSM_ERR_MISALIGNED;
+    const size_t r = size_t(p.requests), t = size_t(p.max_tokens);
+    const Range ins[] = {{p.new_lens, r * 4},
+                         {p.ctx_lens, r * 4},
+                         {p.free_blocks, size_t(p.num_free_blocks) * 4},
+                         {p.free_slots, size_t(p.num_free_slots) * 4}};
+    const Range outs[] = {{p.block_tables, r * size_t(p.max_blocks) * 4},
+                          {p.request_slots, r * 4},
+                          {p.cu_seqlens, (r + 1) * 4},
+                          {p.positions, t * 4},
+                          {p.token_request, t * 4},
+                          {p.slot_map, t * 8},
+                          {p.state_indices, r * 4},
+                          {p.initial_indices, r * 4},
+                          {p.counts, 16}};
+    if (any_overlap(outs, 9, ins, 4)) return JAMBA_SSM_ERR_INVALID_ARG;
+    jamba_ssm_status st;
+    if (!current_device(&st)) return st;
+    jssm::BatchMapsArgs a{};
+    a.requests = static_cast<int>(p.requests);
+    a.max_tokens = static_cast<int>(p.max_tokens);
+    a.max_blocks = static_cast<int>(p.max_blocks);
+    a.block_size = static_cast<int>(p.block_size);
+    a.new_lens = p.new_lens;
+    a.ctx_lens = p.ctx_lens;
+    a.free_blocks = p.free_blocks;
+    a.free_slots = p.free_slots;
+    a.num_free_blocks = static_cast<int>(p.num_free_blocks);
+    a.num_free_slots = static_cast<int>(p.num_free_slots);
+    a.block_tables = p.block_tables;
+    a.request_slots = p.request_slots;
+    a.cu_seqlens = p.cu_seqlens;
+    a.positions = p.positions;
+    a.token_request = p.token_request;
+    a.slot_map = p.slot_map;
+    a.state_indices = p.state_indices;
+    a.initial_indices = p.initial_indices;
+    a.counts = p.counts;
+    void *args[] = {&a};
+    st = launch((const void *)&jssm::batch_maps_simple_kernel, dim3(1), dim3(1), args, 0, stream);
+    return st != JAMBA_SSM_OK ? st : finish_launch(stream, nullptr);
+}
+
+JSSM_SERVE_API jamba_ssm_status jamba_ssm_serve_get_status(void *stream) {
+    return read_status(nullptr, stream);
+}
+JSSM_SERVE_API int jamba_ssm_serve_last_cuda_error(void) { return t_last_cuda_error; }
+JSSM_SERVE_API int jamba_ssm_serve_abi_version(void) { return JAMBA_SSM_SERVE_ABI_VERSION; }

@@ -1,0 +1,254 @@
+"""The maps of a continuous batch on the GPU against a plain loop over requests,
+and a whole serving run: maps, 8-bit projections, packed scans and decode steps."""
+import random
+
+import pytest
+import torch
+
+from selective_state_space_26_b200 import (_lib, jamba_ssm_batch_maps, jamba_ssm_gated_scan,
+                                           jamba_ssm_gated_state_update, jamba_ssm_i8_proj,
+                                           jamba_ssm_i8_quant, jamba_ssm_serve_get_status)
+from tests.gated_ref import Reference, assert_within
+
+pytestmark = pytest.mark.gpu
+
+
+def _i32(v):
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def maps_ref(new, ctx, table, free, slots, free_slots, bs, rows):
+    """The header's definition, request by request; (maps, whether something did not fit)."""
+    width = len(table[0]) if table else 1
+    table, slots = [list(r) for r in table], list(slots)
+    pos, req, smap = [-1] * rows, [-1] * rows, [-1] * rows
+    cu, state, first = [0], [], []
+    blocks = taken = longest = 0
+    bad = False
+    for b, want in enumerate(new):
+        want, c = max(want, 0), max(ctx[b], 0)
+        n = min(want, rows - cu[-1])
+        had = min(-(-c // bs), width)
+        need = -(-(c + n) // bs) if n else had
+        bad |= n < want or need > width
+        for j in range(had, min(need, width)):
+            ok = blocks < len(free)
+            table[b][j] = free[blocks] if ok else -1
+            bad |= not ok
+            blocks += 1
+        if n and c == 0:
+            ok = taken < len(free_slots)
+            slots[b] = free_slots[taken] if ok else -1
+            bad |= not ok
+            taken += 1
+        state.append(slots[b] if n else -1)
+        first.append(slots[b] if n and c else -1)
+        for i in range(n):
+            t, p = cu[-1] + i, c + i
+            blk = table[b][p // bs] if p // bs < width else -1
+            pos[t], req[t] = p, b
+            smap[t] = blk * bs + p % bs if blk >= 0 else -1
+        longest = max(longest, n)
+        cu.append(cu[-1] + n)
+    return {"cu_seqlens": cu, "positions": pos, "token_request": req, "slot_map": smap,
+            "block_tables": table, "request_slots": slots, "state_indices": state,
+            "initial_indices": first,
+            "counts": [cu[-1], min(blocks, len(free)), min(taken, len(free_slots)), longest]}, bad
+
+
+def _run(new, ctx, table, free, slots, free_slots, bs, rows):
+    got = jamba_ssm_batch_maps(_i32(new), _i32(table).view(len(new), -1), _i32(free), _i32(slots),
+                               _i32(free_slots), ctx_lens=None if ctx is None else _i32(ctx),
+                               block_size=bs, max_tokens=rows)
+    return {k: v.tolist() for k, v in got.items()}
+
+
+def _case(rng, requests, most, bs, ctx_most=100, spare=5, rows=None):
+    new = [rng.choice((0, 1, 1, rng.randint(1, most))) for _ in range(requests)]
+    ctx = [rng.choice((0, rng.randint(1, ctx_most))) for _ in range(requests)]
+    width = max([1] + [-(-(c + n) // bs) for c, n in zip(ctx, new)])
+    ids = list(range(requests * width + spare))
+    rng.shuffle(ids)
+    table = [[-1] * width for _ in range(requests)]
+    for b in range(requests):
+        for j in range(-(-ctx[b] // bs)):
+            table[b][j] = ids.pop()
+    slot_ids = list(range(2 * requests + 1))
+    rng.shuffle(slot_ids)
+    slots = [slot_ids.pop() if c else -1 for c in ctx]
+    return new, ctx, table, ids, slots, slot_ids, bs, sum(new) + 7 if rows is None else rows
+
+
+@pytest.mark.parametrize("requests,most,bs", [(1, 1, 16), (1, 300, 16), (3, 40, 1), (31, 20, 7),
+                                              (64, 5, 64), (257, 9, 16), (1000, 30, 32),
+                                              (2500, 3, 16), (70, 1500, 100)])
+def test_maps_match_the_loop(requests, most, bs):
+    args = _case(random.Random(requests + most), requests, most, bs)
+    want, bad = maps_ref(*args)
+    assert not bad
+    assert _run(*args) == want
+    assert jamba_ssm_serve_get_status() == 0
+
+
+def test_no_requests_no_tokens_and_no_context():
+    got = jamba_ssm_batch_maps(_i32([]), _i32([]).view(0, 4), _i32([1]), _i32([]), _i32([]),
+                               max_tokens=5)
+    assert got["cu_seqlens"].tolist() == [0] and got["counts"].tolist() == [0, 0, 0, 0]
+    assert got["slot_map"].tolist() == [-1] * 5 and got["positions"].tolist() == [-1] * 5
+    args = ([0, 0], [5, 0], [[7, 9], [3, 3]], [1], [4, -1], [2], 4, 0)
+    want, _ = maps_ref(*args)
+    assert _run(*args) == want
+    new = [3, 0, 2]
+    want, _ = maps_ref(new, [0] * 3, [[9, 9]] * 3, [1, 2, 3], [-1] * 3, [5, 6], 2, 6)
+    assert _run(new, None, [[9, 9]] * 3, [1, 2, 3], [-1] * 3, [5, 6], 2, 6) == want
+    assert jamba_ssm_serve_get_status() == 0
+
+
+@pytest.mark.parametrize("case", [
+    # tokens past max_tokens: the request in the middle is cut, the ones behind get none
+    ([5, 6, 7, 1], [0, 3, 0, 9], [[0, 0, 0, 0]] * 4, list(range(20, 40)), [-1, 3, -1, 4], [8, 9], 4, 9),
+    # too few free blocks
+    ([9, 9], [0, 0], [[-1] * 3] * 2, [11, 12, 13, 14], [-1, -1], [1, 2], 4, 18),
+    # no free block at all, none of the list
+    ([2], [0], [[-1]], [], [-1], [], 4, 2),
+    # too few state slots
+    ([1, 1, 1], [0, 0, 0], [[-1]] * 3, [1, 2, 3], [-1] * 3, [7], 4, 3),
+    # a request longer than its table; one whose context already is
+    ([9, 2], [0, 20], [[-1, -1], [5, 6]], [1, 2, 3, 4, 5], [-1, 3], [7], 4, 11),
+    # negative lengths count as none; a negative block in the table
+    ([-4, 3, 2], [2, -9, 5], [[1, 1], [-1, -1], [3, -1]], [4, 5, 6], [0, -1, 2], [9], 4, 8),
+])
+def test_what_does_not_fit_is_recorded(case):
+    want, bad = maps_ref(*case)
+    assert _run(*case) == want
+    assert jamba_ssm_serve_get_status() == (_lib.ERR_INVALID_ARG if bad else 0)
+    assert jamba_ssm_serve_get_status() == 0
+
+
+def test_many_requests_and_long_maps():
+    rng = random.Random(4)
+    args = _case(rng, 20000, 6, 8, ctx_most=30)
+    want, bad = maps_ref(*args)
+    assert not bad and _run(*args) == want
+    new, ctx = [200000, 1, 70000], [0, 500000, 3]
+    bs = 1000
+    table = [[-1] * 501 for _ in new]
+    for j in range(500):
+        table[1][j] = 5000 + j
+    table[2][0] = 4999
+    args = (new, ctx, table, list(range(400)), [-1, 0, 1], [5], bs, 270100)
+    want, bad = maps_ref(*args)
+    assert not bad and _run(*args) == want
+
+
+def test_graph_replays_on_new_lengths():
+    rng = random.Random(6)
+    new, ctx, table, free, slots, free_slots, bs, _ = _case(rng, 40, 30, 16)
+    rows = 1300
+    t = {k: _i32(v) for k, v in dict(new=new, ctx=ctx, table=table, free=free, slots=slots,
+                                     fs=free_slots).items()}
+    call = lambda: jamba_ssm_batch_maps(t["new"], t["table"], t["free"], t["slots"], t["fs"],  # noqa: E731
+                                        ctx_lens=t["ctx"], block_size=bs, max_tokens=rows)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = call()
+    fewer = [min(v, 3) for v in new]
+    t["new"].copy_(_i32(fewer))
+    t["table"].copy_(_i32(table))
+    t["slots"].copy_(_i32(slots))
+    graph.replay()
+    torch.cuda.synchronize()
+    want, bad = maps_ref(fewer, ctx, table, free, slots, free_slots, bs, rows)
+    assert not bad and {k: v.tolist() for k, v in got.items()} == want
+
+
+def test_refusals():
+    n = _i32([1, 2])
+    ok = dict(block_tables=_i32([[0], [1]]), free_blocks=n, request_slots=n.clone(), free_slots=n)
+    with pytest.raises(ValueError, match="max_tokens"):
+        jamba_ssm_batch_maps(n, **ok)
+    with pytest.raises(ValueError, match="block_size"):
+        jamba_ssm_batch_maps(n, **ok, max_tokens=3, block_size=0)
+    with pytest.raises(TypeError):
+        jamba_ssm_batch_maps(n.long(), **ok, max_tokens=3)
+    with pytest.raises(ValueError, match="shape"):
+        jamba_ssm_batch_maps(n, **{**ok, "request_slots": _i32([1])}, max_tokens=3)
+    with pytest.raises(ValueError, match="CUDA"):
+        jamba_ssm_batch_maps(n.cpu(), **ok, max_tokens=3)
+    with pytest.raises(_lib.JambaSSMError):  # the slots read are the slots written
+        jamba_ssm_batch_maps(n, **{**ok, "request_slots": ok["free_slots"]}, max_tokens=3)
+
+
+def test_serving_run():
+    """Three steps of a continuous batch through a recurrent layer in 8 bits: the
+    maps, the input projection to x | g | z, the packed scan with state slots, the
+    output projection; then a decode step through the one-token update.  Each
+    request's outputs are those of its tokens alone, from zero."""
+    rng = random.Random(2)
+    gen = torch.Generator(device="cuda")
+    _i32([0])
+    gen.manual_seed(3)
+    d_model, d, requests, bs, width = 96, 64, 5, 8, 16
+    w_in, s_in = jamba_ssm_i8_quant(torch.randn(3 * d, d_model, generator=gen, device="cuda"))
+    w_out, s_out = jamba_ssm_i8_quant(torch.randn(d_model, d, generator=gen, device="cuda"))
+    rate = torch.rand(d, generator=gen, device="cuda")
+    tokens = [torch.randn(60, d_model, generator=gen, device="cuda").to(torch.bfloat16)
+              for _ in range(requests)]
+    cache = torch.full((11, d), 77.0, device="cuda")  # what earlier requests left
+    table = torch.full((requests, width), -1, dtype=torch.int32, device="cuda")
+    slots = torch.full((requests,), -1, dtype=torch.int32, device="cuda")
+    free_b, free_s = rng.sample(range(80), 80), rng.sample(range(11), 11)
+    done = [0] * requests
+    outs = [[] for _ in range(requests)]
+    project = lambda v, w, s: jamba_ssm_i8_proj(*jamba_ssm_i8_quant(v), w, s)  # noqa: E731
+
+    def mixer_inputs(flat):
+        proj = project(flat, w_in, s_in)
+        return proj[:, :d], proj[:, d:2 * d], proj[:, 2 * d:]
+
+    for step in ([20, 0, 9, 1, 33], [5, 17, 0, 1, 2], [1, 1, 30, 1, 0]):
+        flat = torch.cat([tokens[b][done[b]:done[b] + n] for b, n in enumerate(step)])
+        maps = jamba_ssm_batch_maps(_i32(step), table, _i32(free_b), slots, _i32(free_s),
+                                    ctx_lens=_i32(done), block_size=bs, max_tokens=flat.shape[0])
+        x, g, z = mixer_inputs(flat)
+        y, _ = jamba_ssm_gated_scan(x, g, z=z, rate=rate, h0=cache, h_final=cache,
+                                    cu_seqlens=maps["cu_seqlens"],
+                                    state_indices=maps["state_indices"],
+                                    initial_indices=maps["initial_indices"])
+        out = project(y, w_out, s_out)
+        used = maps["counts"].tolist()
+        free_b, free_s = free_b[used[1]:], free_s[used[2]:]
+        at = 0
+        for b, n in enumerate(step):
+            outs[b].append((y[at:at + n], out[at:at + n]))
+            at, done[b] = at + n, done[b] + n
+    # decode: one token each, request 1 paused
+    step = [1, 0, 1, 1, 1]
+    rows = [b for b, n in enumerate(step) if n]
+    maps = jamba_ssm_batch_maps(_i32(step), table, _i32(free_b), slots, _i32(free_s),
+                                ctx_lens=_i32(done), block_size=bs, max_tokens=requests)
+    assert maps["counts"].tolist()[0] == 4
+    x, g, z = mixer_inputs(torch.stack([tokens[b][done[b]] for b in range(requests)]))
+    y = jamba_ssm_gated_state_update(cache, x, g, z=z, rate=rate,
+                                     state_indices=maps["state_indices"])
+    for b in rows:
+        outs[b].append((y[b:b + 1], project(y[b:b + 1], w_out, s_out)))
+        done[b] += 1
+    assert jamba_ssm_serve_get_status() == 0
+    # every block of every table is held once
+    held = [v for r in table.tolist() for v in r if v >= 0]
+    assert len(held) == len(set(held)) == sum(-(-n // bs) for n in done)
+    for b in range(requests):
+        x, g, z = mixer_inputs(tokens[b][:done[b]])
+        ref = Reference(x[None], g[None], z[None], rate)
+        y = torch.cat([v[0] for v in outs[b]])
+        assert_within(y, ref.out, ref.e_out, f"request {b}")
+        assert torch.equal(torch.cat([v[1] for v in outs[b]]), project(y, w_out, s_out))
+        assert_within(cache[int(slots[b])], ref.h_final[0], ref.e_final[0], f"state {b}")
