@@ -67,14 +67,121 @@ jamba_ssm_status launch(const void *k, unsigned grid, unsigned threads, void **a
     return e == cudaSuccess ? JAMBA_SSM_OK : cuda_fail(e);
 }
 
-jamba_ssm_status launch_scan(jssm::GatedArgs &a, int32_t dtype, void *stream) {
-    void *args[] = {&a};
-    const int64_t n = int64_t(a.batch) * a.d;
-    const int64_t grid = (n + 127) / 128;
-    if (grid > 0x7fffffff) return JAMBA_SSM_ERR_UNSUPPORTED;
-    return launch(dtype == JAMBA_SSM_BF16 ? (const void *)&jssm::gated_scan_kernel<__nv_bfloat16>
-                                          : (const void *)&jssm::gated_scan_kernel<float>,
-                  static_cast<unsigned>(grid), 128, args, stream);
+// How the rows can be read: bytes of one copy, the largest of 16, 4 and 2 that
+// divides the width, the strides and every pointer.
+int copy_bytes(const jssm::GatedArgs &a, int32_t dtype) {
+    const int es = dtype == JAMBA_SSM_BF16 ? 2 : 4;
+    int64_t bits = int64_t(a.d) * es;
+    for (int64_t s : {a.xs, a.gs, a.zs}) bits |= s * es;
+    for (const void *p : {a.x, a.g, a.z, (const void *)a.out, a.dout, (const void *)a.dx,
+                          (const void *)a.dg, (const void *)a.dz})
+        bits |= static_cast<int64_t>(reinterpret_cast<uintptr_t>(p));
+    return bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : 2;
+}
+
+// How the work is cut: q runs side by side in a warp, cs CTAs in a cluster.
+struct Cut {
+    int q, cs;
+    int64_t units;  // clusters
+};
+
+// Of a scan over `batch` sequences of about `len` rows of `tiles(q)` channel
+// tiles.  A CTA of q = 1 reads 128 bytes of a row and takes 64 rows a round;
+// q = 2 and 4 halve and quarter the width for two and four times the rows.
+// Measured on 148 SMs (bf16 with z, us):
+//   8192 channels, 4096 rows:  q 1 89, q 2 59, q 4 72, q 2 in clusters of 2 68;
+//   2048 channels, 65536 rows: q 2 in clusters of 8 264, of 4 378, q 4 of 4 303;
+//   512 channels, 8192 rows:   q 4 in clusters of 8 17, q 2 of 8 26, q 1 of 8 37;
+//   13 x 4096 rows x 2048:     q 1 158, q 2 165, in clusters of 8 from 247.
+// So: one CTA to a tile where 2 (q = 1) or 1.5 (q = 2) of them come to an SM;
+// else clusters, whose barrier costs about a round's time and is hidden by the
+// other CTAs of an SM, up to 4 of them; q = 4 where that leaves under 2.
+template <typename Tiles> Cut choose_cut(int64_t batch, int64_t len, int sms, Tiles tiles) {
+    auto clusters = [&](int q) {
+        const int64_t units = batch * tiles(q), rows = int64_t(jssm::kGatedCkpt) * q;
+        int cs = 1;
+        while (cs < jssm::kGatedMaxCluster && cs * 2 <= (len + rows - 1) / rows && units * cs * 2 <= 4 * sms)
+            cs *= 2;
+        return Cut{q, cs, units};
+    };
+    if (batch * tiles(1) >= 2 * sms) return {1, 1, batch * tiles(1)};
+    if (batch * tiles(2) * 2 >= 3 * sms) return {2, 1, batch * tiles(2)};
+    const Cut two = clusters(2);
+    return two.units * two.cs < 2 * sms ? clusters(4) : two;
+}
+
+using Bf = __nv_bfloat16;
+
+struct Kernel {
+    const void *fn;
+    int threads, smem;
+};
+
+// Raises a kernel's dynamic shared-memory limit, once per kernel and device.
+cudaError_t raise_smem(const Kernel &k, int dev) {
+    static std::mutex mutex;
+    static const void *done[kMaxDevices][64];
+    std::lock_guard<std::mutex> lock(mutex);
+    for (const void *&slot : done[dev]) {
+        if (slot == k.fn) return cudaSuccess;
+        if (slot == nullptr) {
+            const cudaError_t e =
+                cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem);
+            if (e == cudaSuccess) slot = k.fn;
+            return e;
+        }
+    }
+    return cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem);
+}
+
+jamba_ssm_status launch_clusters(const Kernel &k, int64_t units, int cs, void **args,
+                                 const DeviceInfo *dev, void *stream) {
+    if (units * cs > 0x7fffffff) return JAMBA_SSM_ERR_UNSUPPORTED;
+    cudaError_t e = raise_smem(k, dev->id);
+    if (e != cudaSuccess) return cuda_fail(e);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(units * cs));
+    cfg.blockDim = dim3(k.threads);
+    cfg.dynamicSmemBytes = k.smem;
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(cs);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cs > 1 ? 1 : 0;
+    e = cudaLaunchKernelExC(&cfg, k.fn, args);
+    return e == cudaSuccess ? JAMBA_SSM_OK : cuda_fail(e);
+}
+
+template <typename T, int VEC, int CP, int Q, bool CL> Kernel scan_kernel_q(bool gate) {
+    return gate ? Kernel{(const void *)&jssm::gated_scan_kernel<T, VEC, true, Q, CP, CL>,
+                         jssm::kGatedThreads, jssm::GatedScanCfg<true>::kSmemBytes}
+                : Kernel{(const void *)&jssm::gated_scan_kernel<T, VEC, false, Q, CP, CL>,
+                         jssm::kGatedThreads, jssm::GatedScanCfg<false>::kSmemBytes};
+}
+template <typename T, int VEC, int CP, bool CL> Kernel scan_kernel_c(bool gate, int q) {
+    return q == 1 ? scan_kernel_q<T, VEC, CP, 1, CL>(gate)
+         : q == 2 ? scan_kernel_q<T, VEC, CP, 2, CL>(gate)
+                  : scan_kernel_q<T, VEC, CP, 4, CL>(gate);
+}
+template <typename T, int VEC, int CP> Kernel scan_kernel(bool gate, int q, int cs) {
+    return cs > 1 ? scan_kernel_c<T, VEC, CP, true>(gate, q) : scan_kernel_c<T, VEC, CP, false>(gate, q);
+}
+
+jamba_ssm_status launch_scan(jssm::GatedArgs &a, int32_t dtype, const DeviceInfo *dev, void *stream) {
+    const int cp = copy_bytes(a, dtype);
+    const bool bf = dtype == JAMBA_SSM_BF16, gate = a.z != nullptr;
+    const int width = bf && cp >= 4 ? 64 : 32;  // channels of a warp's row
+    const Cut cut = choose_cut(a.batch, a.cu ? a.total / a.batch : a.seqlen, dev->sms,
+                               [&](int q) { return int64_t(a.d + width / q - 1) / (width / q); });
+    int q = cut.q, cs = cut.cs;
+    void *args[] = {&a, &cs};
+    const Kernel k = !bf ? (cp == 16 ? scan_kernel<float, 1, 16>(gate, q, cs) : scan_kernel<float, 1, 4>(gate, q, cs))
+                     : cp == 16 ? scan_kernel<Bf, 2, 16>(gate, q, cs)
+                     : cp == 4  ? scan_kernel<Bf, 2, 4>(gate, q, cs)
+                                : scan_kernel<Bf, 1, 2>(gate, q, cs);
+    return launch_clusters(k, cut.units, cs, args, dev, stream);
 }
 
 size_t ckpt_bytes(int64_t batch, int64_t rows, int64_t d) {
@@ -127,7 +234,8 @@ JSSM_GATED_API jamba_ssm_status jamba_ssm_gated_scan(const jamba_ssm_gated_scan_
                           {p.ckpt, ckpt_bytes(p.batch, rows, p.d_inner)},
                           {p.workspace, size_t(JAMBA_SSM_STATUS_BYTES)}};
     if (any_overlap(outs, 4, ins, 9)) return JAMBA_SSM_ERR_INVALID_ARG;
-    if (!current_device(&st)) return st;
+    const DeviceInfo *dev = current_device(&st);
+    if (!dev) return st;
 
     jssm::GatedArgs a{};
     fill_common(p, rows, &a);
@@ -138,7 +246,7 @@ JSSM_GATED_API jamba_ssm_status jamba_ssm_gated_scan(const jamba_ssm_gated_scan_
     a.num_slots = p.num_slots;
     a.ckpt = p.ckpt;
     a.status = static_cast<int *>(p.workspace);
-    if ((st = launch_scan(a, p.io_dtype, stream)) != JAMBA_SSM_OK) return st;
+    if ((st = launch_scan(a, p.io_dtype, dev, stream)) != JAMBA_SSM_OK) return st;
     return finish_launch(stream, p.workspace);
 }
 
@@ -174,7 +282,8 @@ jamba_ssm_gated_scan_bwd(const jamba_ssm_gated_scan_bwd_params *pin, void *strea
     const Range outs[] = {{p.dx, act},   {p.dg, act},    {p.dz, act},   {p.drate, par},
                           {p.dbias, par}, {p.dh0, state}, {p.workspace, need}};
     if (any_overlap(outs, 7, ins, 10)) return JAMBA_SSM_ERR_INVALID_ARG;
-    if (!current_device(&st)) return st;
+    const DeviceInfo *dev = current_device(&st);
+    if (!dev) return st;
 
     jssm::GatedArgs a{};
     fill_common(p, rows, &a);
@@ -192,7 +301,7 @@ jamba_ssm_gated_scan_bwd(const jamba_ssm_gated_scan_bwd_params *pin, void *strea
     if (p.batch > 0) {
         if (!a.ckpt) {
             a.ckpt = a.partial + partial_bytes(p.batch, p.d_inner) / 4;
-            if ((st = launch_scan(a, p.io_dtype, stream)) != JAMBA_SSM_OK) return st;
+            if ((st = launch_scan(a, p.io_dtype, dev, stream)) != JAMBA_SSM_OK) return st;
         }
         const int64_t grid = (p.batch * p.d_inner + 127) / 128;
         if (grid > 0x7fffffff) return JAMBA_SSM_ERR_UNSUPPORTED;

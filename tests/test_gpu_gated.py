@@ -54,6 +54,32 @@ def test_scan_matches_recurrence(dtype, batch, seqlen, d):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("batch,seqlen,d", [(40, 150, 512), (24, 300, 320), (2, 700, 2048)])
+def test_scan_of_many_tiles(dtype, batch, seqlen, d):
+    """Enough channel tiles for the whole device: the cuts without clusters."""
+    x, g, z, rate, bias = _inputs((batch, seqlen, d), dtype, d)
+    h0 = torch.randn(batch, d, device=x.device)
+    out, hf = jamba_ssm_gated_scan(x, g, z=z, rate=rate, bias=bias, h0=h0)
+    _check_scan(Reference(x, g, z, rate, bias, h0), out, hf, f"{batch}x{seqlen}x{d}")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_gates_whose_product_leaves_the_range(dtype):
+    """Neighbouring channels closed to e^-50 each: their exponentials' product is
+    past fp32, and the small rates must come out as they are, not as 0."""
+    x, g, z, rate, bias = _inputs((1, 200, 64), dtype, 2)
+    g[:] = -50.0
+    z[:, :, ::2] = -60.0
+    rate[:] = 1.0
+    out, hf = jamba_ssm_gated_scan(x, g, z=z, rate=rate)
+    ref = Reference(x, g, z, rate)
+    _check_scan(ref, out, hf, "closed pairs")
+    assert (hf != 0).all()
+    rel = (hf.double().cpu() - ref.h_final).norm() / ref.h_final.norm()
+    assert rel < 200 * 2.0 ** -22  # each rate is within (50 + 8) 2^-23, each sum 2^-24
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 def test_scan_optional_arguments(dtype):
     x, g, z, rate, bias = _inputs((2, 100, 40), dtype, 3)
     out, hf = jamba_ssm_gated_scan(x, g)
