@@ -48,23 +48,95 @@ __device__ __forceinline__ I8Scale i8_scale(uint32_t amax_bits) {
     return r;
 }
 
-template <typename T> __global__ void i8_quant_kernel(const I8QuantArgs a) {
-    __shared__ uint32_t part[4];
-    const int64_t row = blockIdx.x;
-    const T *x = static_cast<const T *>(a.x) + row * a.xs;
+// Eight neighbouring elements; those from n on read as 0.
+template <bool VECTOR> __device__ __forceinline__ void i8_load8(const __nv_bfloat16 *p, int n, float (&v)[8]) {
+    if (VECTOR && n >= 8) {
+        const uint4 r = *reinterpret_cast<const uint4 *>(p);
+        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = __uint_as_float(w[i] << 16);
+            v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = i < n ? __bfloat162float(p[i]) : 0.0f;
+    }
+}
+template <bool VECTOR> __device__ __forceinline__ void i8_load8(const float *p, int n, float (&v)[8]) {
+    if (VECTOR && n >= 8) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float4 r = reinterpret_cast<const float4 *>(p)[i];
+            v[4 * i] = r.x, v[4 * i + 1] = r.y, v[4 * i + 2] = r.z, v[4 * i + 3] = r.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = i < n ? p[i] : 0.0f;
+    }
+}
+
+// LANES threads take a row, eight elements at a time; the first kKept of a
+// thread's eights stay in registers between the two passes (every row of up to
+// 8 * LANES * kKept elements is read once), the others are read again, from L2.
+// VECTOR: rows begin at 16-byte boundaries.
+constexpr int kQuantThreads = 256, kQuantKept = 4;
+template <typename T, int LANES, bool VECTOR>
+__global__ void __launch_bounds__(kQuantThreads) i8_quant_kernel(const I8QuantArgs a) {
+    __shared__ uint32_t part[kQuantThreads / 32];
+    const int64_t row = int64_t(blockIdx.x) * (kQuantThreads / LANES) + threadIdx.x / LANES;
+    const int l = threadIdx.x % LANES;
+    const bool on = row < a.rows;
+    const T *x = static_cast<const T *>(a.x) + (on ? row : 0) * a.xs;
+    const int k = on ? a.k : 0;
+    float kept[kQuantKept][8];
     uint32_t m = 0;
-    for (int c = threadIdx.x; c < a.k; c += 128)
-        m = max(m, __float_as_uint(to_f32(x[c])) & 0x7fffffffu);
+    auto most = [&](const float (&v)[8]) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
+    };
+#pragma unroll
+    for (int j = 0; j < kQuantKept; ++j) {
+        const int c = (j * LANES + l) * 8;
+        i8_load8<VECTOR>(x + c, k - c, kept[j]);
+        most(kept[j]);
+    }
+    for (int c = (kQuantKept * LANES + l) * 8; c < k; c += LANES * 8) {
+        float v[8];
+        i8_load8<VECTOR>(x + c, k - c, v);
+        most(v);
+    }
     m = __reduce_max_sync(0xffffffffu, m);
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
-    __syncthreads();
-    m = max(max(part[0], part[1]), max(part[2], part[3]));
+    if constexpr (LANES > 32) {
+        if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
+        __syncthreads();
+        const int w0 = threadIdx.x / LANES * (LANES / 32);
+#pragma unroll
+        for (int w = 0; w < LANES / 32; ++w) m = max(m, part[w0 + w]);
+    }
+    if (!on) return;
     const I8Scale sc = i8_scale(m);
-    if (threadIdx.x == 0) a.scale[row] = sc.scale;
+    if (l == 0) a.scale[row] = sc.scale;
     int8_t *q = a.q + row * a.pitch;
-    for (int c = threadIdx.x; c < a.pitch; c += 128)
-        q[c] = c < a.k && !sc.zero ? static_cast<int8_t>(i8_round(to_f32(x[c]) * sc.up, sc.s, sc.inv))
-                                   : int8_t(0);
+    auto put = [&](int c, const float (&v)[8]) {
+        uint32_t w[2] = {0, 0};
+        if (!sc.zero) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                w[i / 4] |= (uint32_t(i8_round(v[i] * sc.up, sc.s, sc.inv)) & 0xffu) << (8 * (i % 4));
+        }
+        *reinterpret_cast<uint2 *>(q + c) = make_uint2(w[0], w[1]);
+    };
+#pragma unroll
+    for (int j = 0; j < kQuantKept; ++j) {
+        const int c = (j * LANES + l) * 8;
+        if (c < a.pitch) put(c, kept[j]);
+    }
+    for (int c = (kQuantKept * LANES + l) * 8; c < a.pitch; c += LANES * 8) {
+        float v[8];
+        i8_load8<VECTOR>(x + c, k - c, v);
+        put(c, v);
+    }
 }
 
 }  // namespace jssm

@@ -17,11 +17,90 @@ using namespace jssm_host;
 namespace {
 
 constexpr int64_t kMaxRows = (int64_t(1) << 31) - (int64_t(1) << 16);
+constexpr uint64_t kDefaultTimeoutCycles = 4000000000ull;  // about 2 s
 
 jamba_ssm_status launch(const void *k, dim3 grid, dim3 threads, void **args, size_t smem, void *stream) {
     cudaError_t e = cudaLaunchKernel(k, grid, threads, args, smem, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? JAMBA_SSM_OK : cuda_fail(e);
 }
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                                   const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                                   const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn(jamba_ssm_status *st) {
+    static EncodeTiledFn fn = nullptr;
+    static std::once_flag once;
+    static cudaError_t err = cudaSuccess;
+    std::call_once(once, [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        err = cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q);
+        if (err == cudaSuccess && q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeTiledFn>(p);
+        else if (err == cudaSuccess)
+            err = cudaErrorSymbolNotFound;
+    });
+    if (!fn) *st = cuda_fail(err);
+    return fn;
+}
+
+// Map over [rows][pitch] bytes, box of 128 bytes x box_rows, 128-byte swizzle,
+// zeros outside the tensor.
+bool encode_bytes(EncodeTiledFn fn, CUtensorMap *map, const void *ptr, int64_t pitch, int64_t rows,
+                  int box_rows) {
+    cuuint64_t dims[2] = {(cuuint64_t)pitch, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)pitch};
+    cuuint32_t box[2] = {128, (cuuint32_t)box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(ptr), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct Kernel {
+    const void *fn;
+    int smem;
+};
+
+// Raises a kernel's dynamic shared-memory limit, once per kernel and device.
+cudaError_t raise_smem(const Kernel &k, int dev) {
+    static std::mutex mutex;
+    static const void *done[kMaxDevices][16];
+    std::lock_guard<std::mutex> lock(mutex);
+    for (const void *&slot : done[dev]) {
+        if (slot == k.fn) return cudaSuccess;
+        if (slot == nullptr) {
+            const cudaError_t e =
+                cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem);
+            if (e == cudaSuccess) slot = k.fn;
+            return e;
+        }
+    }
+    return cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem);
+}
+
+template <typename T, int LANES> const void *quant_kernel_l(bool vec) {
+    return vec ? (const void *)&jssm::i8_quant_kernel<T, LANES, true>
+               : (const void *)&jssm::i8_quant_kernel<T, LANES, false>;
+}
+template <typename T> const void *quant_kernel(int lanes, bool vec) {
+    return lanes == 32 ? quant_kernel_l<T, 32>(vec)
+         : lanes == 128 ? quant_kernel_l<T, 128>(vec)
+                        : quant_kernel_l<T, 256>(vec);
+}
+
+template <typename T> Kernel split_kernel(int nt) {
+    switch (nt) {
+        case 16: return {(const void *)&jssm::i8_proj_split_kernel<T, 16>, jssm::I8SplitCfg<16>::kSmem};
+        case 32: return {(const void *)&jssm::i8_proj_split_kernel<T, 32>, jssm::I8SplitCfg<32>::kSmem};
+        case 64: return {(const void *)&jssm::i8_proj_split_kernel<T, 64>, jssm::I8SplitCfg<64>::kSmem};
+        default: return {(const void *)&jssm::i8_proj_split_kernel<T, 128>, jssm::I8SplitCfg<128>::kSmem};
+    }
+}
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 bool io_dtype(int32_t d) { return d == JAMBA_SSM_BF16 || d == JAMBA_SSM_F32; }
 
@@ -54,9 +133,14 @@ JSSM_SERVE_API jamba_ssm_status jamba_ssm_i8_quant(const jamba_ssm_i8_quant_para
     a.k = static_cast<int>(p.k);
     a.pitch = static_cast<int>(pitch);
     void *args[] = {&a};
-    st = launch(p.x_dtype == JAMBA_SSM_BF16 ? (const void *)&jssm::i8_quant_kernel<__nv_bfloat16>
-                                            : (const void *)&jssm::i8_quant_kernel<float>,
-                dim3(unsigned(p.rows)), dim3(128), args, 0, stream);
+    // the fewest threads that keep the whole row in registers
+    const int per = 8 * jssm::kQuantKept;
+    const int lanes = p.k <= 32 * per ? 32 : p.k <= 128 * per ? 128 : 256;
+    const bool vec = aligned(p.x, 16) && p.x_stride * es % 16 == 0;
+    const void *k = p.x_dtype == JAMBA_SSM_BF16 ? quant_kernel<__nv_bfloat16>(lanes, vec)
+                                                : quant_kernel<float>(lanes, vec);
+    st = launch(k, dim3(unsigned(ceil_div(p.rows, jssm::kQuantThreads / lanes))),
+                dim3(jssm::kQuantThreads), args, 0, stream);
     return st != JAMBA_SSM_OK ? st : finish_launch(stream, nullptr);
 }
 
@@ -82,29 +166,58 @@ JSSM_SERVE_API jamba_ssm_status jamba_ssm_i8_proj(const jamba_ssm_i8_proj_params
     const Range outs[] = {{p.out, size_t(p.ntok) * p.n_out * es}};
     if (any_overlap(outs, 1, ins, 5)) return JAMBA_SSM_ERR_INVALID_ARG;
     jamba_ssm_status st;
-    if (!current_device(&st)) return st;
+    const DeviceInfo *dev = current_device(&st);
+    if (!dev) return st;
+    EncodeTiledFn fn = encode_fn(&st);
+    if (!fn) return st;
     jssm::I8ProjArgs a{};
-    a.q = p.q;
-    a.w = p.w;
     a.qs = p.q_scale;
     a.ws = p.w_scale;
     a.bias = p.bias;
     a.out = p.out;
+    a.ntok = static_cast<int>(p.ntok);
     a.n = static_cast<int>(p.n_out);
-    a.pitch = static_cast<int>(pitch);
-    void *args[] = {&a};
-    // at most 65535 x 8 tokens fit one grid
-    for (int64_t t = 0; t < p.ntok; t += 65535 * 8) {
-        a.ntok = p.ntok - t < 65535 * 8 ? p.ntok - t : 65535 * 8;
-        a.q = p.q + t * pitch;
-        a.qs = p.q_scale + t;
-        a.out = static_cast<char *>(p.out) + size_t(t) * p.n_out * es;
-        st = launch(p.out_dtype == JAMBA_SSM_BF16 ? (const void *)&jssm::i8_proj_simple_kernel<__nv_bfloat16>
-                                                  : (const void *)&jssm::i8_proj_simple_kernel<float>,
-                    dim3(unsigned((p.n_out + 31) / 32), unsigned((a.ntok + 7) / 8)), dim3(32, 8), args, 0,
-                    stream);
-        if (st != JAMBA_SSM_OK) return st;
+    a.kblocks = static_cast<int>(ceil_div(pitch, 128));
+    a.limit = p.timeout_cycles ? p.timeout_cycles : kDefaultTimeoutCycles;
+    const bool bf = p.out_dtype == JAMBA_SSM_BF16;
+    CUtensorMap map_w, map_q;
+    if (!encode_bytes(fn, &map_w, p.w, pitch, p.n_out, 128)) return cuda_fail(cudaErrorInvalidValue);
+
+    const int64_t pair_tiles = ceil_div(p.n_out, 256) * ceil_div(p.ntok, 256);
+    const bool pair = p.ntok > 128 && pair_tiles * 4 >= dev->sms;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.blockDim = dim3(192);
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    Kernel k;
+    if (pair) {
+        if (!encode_bytes(fn, &map_q, p.q, pitch, p.ntok, 128)) return cuda_fail(cudaErrorInvalidValue);
+        k = bf ? Kernel{(const void *)&jssm::i8_proj_pair_kernel<__nv_bfloat16>, jssm::I8PairCfg::kSmem}
+               : Kernel{(const void *)&jssm::i8_proj_pair_kernel<float>, jssm::I8PairCfg::kSmem};
+        const int64_t pairs = dev->sms / 2;
+        cfg.gridDim = dim3(unsigned(2 * (pair_tiles < pairs ? pair_tiles : pairs)));
+        cfg.numAttrs = 0;  // the kernel's own cluster of 2
+    } else {
+        const int nt = p.ntok <= 16 ? 16 : p.ntok <= 32 ? 32 : p.ntok <= 64 ? 64 : 128;
+        if (!encode_bytes(fn, &map_q, p.q, pitch, p.ntok, nt)) return cuda_fail(cudaErrorInvalidValue);
+        k = bf ? split_kernel<__nv_bfloat16>(nt) : split_kernel<float>(nt);
+        const int64_t tiles = ceil_div(p.n_out, 128) * ceil_div(p.ntok, nt);
+        a.ks = 1;
+        while (a.ks < jssm::kI8MaxSplit && a.ks * 2 <= a.kblocks && tiles * a.ks * 2 <= dev->sms) a.ks *= 2;
+        if (tiles * a.ks > 0x7fffffff) return JAMBA_SSM_ERR_UNSUPPORTED;
+        cfg.gridDim = dim3(unsigned(tiles * a.ks));
+        attr[0].val.clusterDim.x = unsigned(a.ks);
+        cfg.numAttrs = a.ks > 1 ? 1 : 0;
     }
+    cudaError_t e = raise_smem(k, dev->id);
+    if (e != cudaSuccess) return cuda_fail(e);
+    cfg.dynamicSmemBytes = k.smem;
+    void *args[] = {&map_w, &map_q, &a};
+    e = cudaLaunchKernelExC(&cfg, k.fn, args);
+    if (e != cudaSuccess) return cuda_fail(e);
     return finish_launch(stream, nullptr);
 }
 
