@@ -134,4 +134,27 @@ inline jamba_ssm_status finish_launch(void *stream, void *workspace) {
     return sync_check ? read_status(workspace, stream) : JAMBA_SSM_OK;
 }
 
+// Launches `k`, its clusters `cs` CTAs along x, and lets it begin while the work
+// before it in the stream ends: such a kernel touches no memory before its
+// griddepcontrol.wait (jssm::after_earlier_work), so only its own start -- the
+// launch itself, barriers, TMEM -- overlaps.
+inline jamba_ssm_status launch_early(const void *k, dim3 grid, unsigned threads, size_t smem, int cs,
+                                     void **args, void *stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(cs);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cs > 1 ? 2 : 1;
+    const cudaError_t e = cudaLaunchKernelExC(&cfg, k, args);
+    return e == cudaSuccess ? JAMBA_SSM_OK : cuda_fail(e);
+}
+
 }  // namespace jssm_host

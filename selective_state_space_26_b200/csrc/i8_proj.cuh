@@ -10,6 +10,7 @@
 #pragma once
 
 #include "device_utils.cuh"
+#include "launch_order.cuh"
 #include "tcgen05_utils.cuh"
 
 namespace jssm {
@@ -181,6 +182,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(I8PairCfg::kThreads,
     __syncthreads();
     cluster_barrier();
     tc_fence_after();
+    after_earlier_work();
+    let_next_begin();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(tmem_slot);
 
     if (warp == 0) {
@@ -331,11 +334,15 @@ __global__ void __launch_bounds__(I8SplitCfg<NT>::kThreads, 1)
         mbar_init(acc_full, 1);
         *abort_flag = 0;
         fence_mbarrier_init();
+        prefetch_tensormap(&map_w);
+        prefetch_tensormap(&map_q);
     }
     if (warp == 1) {
         tmem_alloc(tmem_slot, C::kTmemCols);
         tmem_relinquish();
     }
+    after_earlier_work();
+    let_next_begin();
     for (int i = threadIdx.x; i < NT; i += C::kThreads) scales[i] = m0 + i < a.ntok ? a.qs[m0 + i] : 0.0f;
     tc_fence_before();
     __syncthreads();
@@ -399,32 +406,65 @@ __global__ void __launch_bounds__(I8SplitCfg<NT>::kThreads, 1)
             }
         }
     } else {
-        // column c is finished by CTA c % ks, in its slots [c / ks][source rank]
-        int *sums = reinterpret_cast<int *>(smem);
+        // CTA r finishes the columns from r * own on, in pairs and fours of columns:
+        // slot [group][source rank][channel][column of the group]
+        uint8_t *sums = smem;
+        const int own = NT / a.ks, log_own = __ffs(own) - 1;
         cluster_barrier();  // every CTA's stages are free
         if (warp >= 2) {
+            const int width = own >= 4 ? 4 : 2;  // columns of a group
+            const uint32_t at = smem_u32(sums) + (rank * C::kM + q * 32 + lane) * width * 4;
+            const uint32_t group = a.ks * C::kM * width * 4;
 #pragma unroll 1
-            for (int c = 0; c < NT; c += 16) {
+            for (int c = 0; c < cols; c += 16) {
                 uint32_t v[16];
                 tmem_ld16_async(lanes + c, v);
                 tmem_wait_ld();
                 tmem_regs_ready(v);
+                if (own >= 4) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int owner = (c + i) % a.ks;
-                    if (c + i >= cols) continue;
-                    const uint32_t at =
-                        smem_u32(sums + (((c + i) / a.ks) * a.ks + rank) * C::kM + q * 32 + lane);
-                    asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(mapa(at, owner)), "r"(v[i]) : "memory");
+                    for (int i = 0; i < 16; i += 4) {
+                        const uint32_t to = mapa(at + (((c + i) & (own - 1)) >> 2) * group, (c + i) >> log_own);
+                        asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(v[i]),
+                                     "r"(v[i + 1]), "r"(v[i + 2]), "r"(v[i + 3])
+                                     : "memory");
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16; i += 2)
+                        asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(mapa(at, (c + i) >> 1)),
+                                     "r"(v[i]), "r"(v[i + 1])
+                                     : "memory");
                 }
             }
         }
         cluster_barrier();
         if (warp >= 2 && on) {
-            for (int c = rank; c < cols; c += a.ks) {
-                int acc = 0;
-                for (int r = 0; r < a.ks; ++r) acc += sums[((c / a.ks) * a.ks + r) * C::kM + q * 32 + lane];
-                i8_put<T>(out + int64_t(c) * a.n, acc, scales[c], w, bias);
+            const int c0 = rank * own, end = min(c0 + own, cols);
+            if (own >= 4) {
+                const int4 *mine = reinterpret_cast<const int4 *>(sums) + q * 32 + lane;
+                for (int c = c0; c < end; c += 4) {
+                    int4 t = make_int4(0, 0, 0, 0);
+                    for (int r = 0; r < a.ks; ++r) {
+                        const int4 p = mine[r * C::kM];
+                        t.x += p.x, t.y += p.y, t.z += p.z, t.w += p.w;
+                    }
+                    mine += a.ks * C::kM;
+                    const int acc[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (c + i < end)
+                            i8_put<T>(out + int64_t(c + i) * a.n, acc[i], scales[c + i], w, bias);
+                }
+            } else {
+                const int2 *mine = reinterpret_cast<const int2 *>(sums) + q * 32 + lane;
+                int2 t = make_int2(0, 0);
+                for (int r = 0; r < a.ks; ++r) {
+                    const int2 p = mine[r * C::kM];
+                    t.x += p.x, t.y += p.y;
+                }
+                if (c0 < end) i8_put<T>(out + int64_t(c0) * a.n, t.x, scales[c0], w, bias);
+                if (c0 + 1 < end) i8_put<T>(out + int64_t(c0 + 1) * a.n, t.y, scales[c0 + 1], w, bias);
             }
         }
     }

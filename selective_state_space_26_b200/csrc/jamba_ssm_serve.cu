@@ -139,8 +139,8 @@ JSSM_SERVE_API jamba_ssm_status jamba_ssm_i8_quant(const jamba_ssm_i8_quant_para
     const bool vec = aligned(p.x, 16) && p.x_stride * es % 16 == 0;
     const void *k = p.x_dtype == JAMBA_SSM_BF16 ? quant_kernel<__nv_bfloat16>(lanes, vec)
                                                 : quant_kernel<float>(lanes, vec);
-    st = launch(k, dim3(unsigned(ceil_div(p.rows, jssm::kQuantThreads / lanes))),
-                dim3(jssm::kQuantThreads), args, 0, stream);
+    st = launch_early(k, dim3(unsigned(ceil_div(p.rows, jssm::kQuantThreads / lanes))),
+                      jssm::kQuantThreads, 0, 1, args, stream);
     return st != JAMBA_SSM_OK ? st : finish_launch(stream, nullptr);
 }
 
@@ -185,21 +185,15 @@ JSSM_SERVE_API jamba_ssm_status jamba_ssm_i8_proj(const jamba_ssm_i8_proj_params
 
     const int64_t pair_tiles = ceil_div(p.n_out, 256) * ceil_div(p.ntok, 256);
     const bool pair = p.ntok > 128 && pair_tiles * 4 >= dev->sms;
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.blockDim = dim3(192);
-    cfg.stream = static_cast<cudaStream_t>(stream);
     Kernel k;
+    int64_t grid;
     if (pair) {
         if (!encode_bytes(fn, &map_q, p.q, pitch, p.ntok, 128)) return cuda_fail(cudaErrorInvalidValue);
         k = bf ? Kernel{(const void *)&jssm::i8_proj_pair_kernel<__nv_bfloat16>, jssm::I8PairCfg::kSmem}
                : Kernel{(const void *)&jssm::i8_proj_pair_kernel<float>, jssm::I8PairCfg::kSmem};
         const int64_t pairs = dev->sms / 2;
-        cfg.gridDim = dim3(unsigned(2 * (pair_tiles < pairs ? pair_tiles : pairs)));
-        cfg.numAttrs = 0;  // the kernel's own cluster of 2
+        grid = 2 * (pair_tiles < pairs ? pair_tiles : pairs);
+        a.ks = 1;  // the kernel has its own cluster of 2
     } else {
         const int nt = p.ntok <= 16 ? 16 : p.ntok <= 32 ? 32 : p.ntok <= 64 ? 64 : 128;
         if (!encode_bytes(fn, &map_q, p.q, pitch, p.ntok, nt)) return cuda_fail(cudaErrorInvalidValue);
@@ -207,18 +201,14 @@ JSSM_SERVE_API jamba_ssm_status jamba_ssm_i8_proj(const jamba_ssm_i8_proj_params
         const int64_t tiles = ceil_div(p.n_out, 128) * ceil_div(p.ntok, nt);
         a.ks = 1;
         while (a.ks < jssm::kI8MaxSplit && a.ks * 2 <= a.kblocks && tiles * a.ks * 2 <= dev->sms) a.ks *= 2;
-        if (tiles * a.ks > 0x7fffffff) return JAMBA_SSM_ERR_UNSUPPORTED;
-        cfg.gridDim = dim3(unsigned(tiles * a.ks));
-        attr[0].val.clusterDim.x = unsigned(a.ks);
-        cfg.numAttrs = a.ks > 1 ? 1 : 0;
+        grid = tiles * a.ks;
+        if (grid > 0x7fffffff) return JAMBA_SSM_ERR_UNSUPPORTED;
     }
-    cudaError_t e = raise_smem(k, dev->id);
+    const cudaError_t e = raise_smem(k, dev->id);
     if (e != cudaSuccess) return cuda_fail(e);
-    cfg.dynamicSmemBytes = k.smem;
     void *args[] = {&map_w, &map_q, &a};
-    e = cudaLaunchKernelExC(&cfg, k.fn, args);
-    if (e != cudaSuccess) return cuda_fail(e);
-    return finish_launch(stream, nullptr);
+    st = launch_early(k.fn, dim3(unsigned(grid)), 192, k.smem, a.ks, args, stream);
+    return st != JAMBA_SSM_OK ? st : finish_launch(stream, nullptr);
 }
 
 JSSM_SERVE_API jamba_ssm_status jamba_ssm_batch_maps(const jamba_ssm_batch_maps_params *pin, void *stream) {
