@@ -79,7 +79,15 @@ def launching(stream, device):
 
 
 def raw_stream(device):
-    return torch.cuda.current_stream(device).cuda_stream
+    """The device's current stream, without making a Stream object for it."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def empty_like(t, contiguous=True):
+    """An uninitialised contiguous tensor like t (`contiguous`: whether t is)."""
+    if contiguous:
+        return torch.empty_like(t)
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
 def workspace(ws, device):

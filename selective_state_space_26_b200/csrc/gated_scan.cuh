@@ -595,37 +595,4 @@ __global__ void gated_reduce_kernel(const float *partial, float *drate, float *d
     if (dbias) dbias[c] = s;
 }
 
-// One token for each request, one thread for each channel of it.
-struct GatedUpdateArgs {
-    float *state;
-    const void *x, *g, *z;
-    int64_t xs, gs, zs;
-    const float *rate, *bias;
-    void *out;
-    const int32_t *state_indices;
-    int64_t num_slots;
-    int *status;
-    int d, batch;
-};
-template <typename T> __global__ void gated_update_kernel(const GatedUpdateArgs a) {
-    const int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;
-    const int64_t b = i / a.d;
-    const int c = static_cast<int>(i % a.d);
-    if (b >= a.batch) return;
-    int64_t row = b;
-    if (a.state_indices) {
-        row = a.state_indices[b];
-        if (row >= a.num_slots && c == 0) record_status(a.status, kStInvalidArg);
-        if (row < 0 || row >= a.num_slots) return;
-    }
-    const float u = (a.rate ? a.rate[c] : 1.0f) *
-                    sigmoid_f32(to_f32(static_cast<const T *>(a.g)[b * a.gs + c]) +
-                                (a.bias ? a.bias[c] : 0.0f));
-    float h = a.state[row * a.d + c];
-    h = fmaf(u, to_f32(static_cast<const T *>(a.x)[b * a.xs + c]) - h, h);
-    a.state[row * a.d + c] = h;
-    static_cast<T *>(a.out)[b * a.d + c] =
-        from_f32<T>(a.z ? h * silu_f32(to_f32(static_cast<const T *>(a.z)[b * a.zs + c])) : h);
-}
-
 }  // namespace jssm

@@ -5,6 +5,7 @@
 #include "jamba_ssm_gated.h"
 
 #include "gated_scan.cuh"
+#include "gated_update.cuh"
 #include "host_utils.h"
 
 #define JSSM_GATED_API extern "C" __attribute__((visibility("default")))
@@ -371,11 +372,22 @@ jamba_ssm_gated_state_update(const jamba_ssm_gated_state_update_params *pin, voi
     a.d = static_cast<int>(p.d_inner);
     a.batch = static_cast<int>(p.batch);
     void *args[] = {&a};
-    const int64_t grid = (p.batch * p.d_inner + 255) / 256;
-    if (grid > 0x7fffffff) return JAMBA_SSM_ERR_UNSUPPORTED;
-    st = launch(p.io_dtype == JAMBA_SSM_BF16 ? (const void *)&jssm::gated_update_kernel<__nv_bfloat16>
-                                             : (const void *)&jssm::gated_update_kernel<float>,
-                static_cast<unsigned>(grid), 256, args, stream);
+    // 16-byte rows throughout: 8 bf16 or 4 fp32 channels a thread
+    const int v = p.io_dtype == JAMBA_SSM_BF16 ? 8 : 4;
+    bool wide = p.d_inner % v == 0;
+    for (int64_t s : {p.x_stride, p.g_stride, p.z_stride}) wide = wide && s % v == 0;
+    for (const void *q : {p.x, p.g, p.z, (const void *)p.out, (const void *)p.state,
+                          (const void *)p.rate, (const void *)p.bias})
+        wide = wide && aligned(q, 16);
+    const void *k = p.io_dtype == JAMBA_SSM_BF16
+                        ? (wide ? (const void *)&jssm::gated_update_kernel<Bf, 8>
+                                : (const void *)&jssm::gated_update_kernel<Bf, 1>)
+                        : (wide ? (const void *)&jssm::gated_update_kernel<float, 4>
+                                : (const void *)&jssm::gated_update_kernel<float, 1>);
+    const int64_t per = int64_t(jssm::kUpdateThreads) * (wide ? v : 1);
+    const dim3 grid(static_cast<unsigned>((p.d_inner + per - 1) / per),
+                    static_cast<unsigned>(p.batch < 65535 ? p.batch : 65535));
+    st = launch_early(k, grid, jssm::kUpdateThreads, 0, 1, args, stream);
     if (st != JAMBA_SSM_OK) return st;
     return finish_launch(stream, p.workspace);
 }

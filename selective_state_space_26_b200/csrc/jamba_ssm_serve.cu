@@ -19,11 +19,6 @@ namespace {
 constexpr int64_t kMaxRows = (int64_t(1) << 31) - (int64_t(1) << 16);
 constexpr uint64_t kDefaultTimeoutCycles = 4000000000ull;  // about 2 s
 
-jamba_ssm_status launch(const void *k, dim3 grid, dim3 threads, void **args, size_t smem, void *stream) {
-    cudaError_t e = cudaLaunchKernel(k, grid, threads, args, smem, static_cast<cudaStream_t>(stream));
-    return e == cudaSuccess ? JAMBA_SSM_OK : cuda_fail(e);
-}
-
 using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
                                    const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
                                    const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
@@ -274,8 +269,22 @@ JSSM_SERVE_API jamba_ssm_status jamba_ssm_batch_maps(const jamba_ssm_batch_maps_
     a.state_indices = p.state_indices;
     a.initial_indices = p.initial_indices;
     a.counts = p.counts;
+    a.wide = aligned(p.positions, 16) && aligned(p.token_request, 16) && aligned(p.slot_map, 16);
     void *args[] = {&a};
-    st = launch((const void *)&jssm::batch_maps_simple_kernel, dim3(1), dim3(1), args, 0, stream);
+    const unsigned ctas =
+        unsigned(ceil_div(p.max_tokens, int64_t(jssm::kMapsThreads) * jssm::kMapsTokens));
+    if (p.requests <= jssm::kMapsFused) {
+        const void *k = p.requests <= jssm::kMapsThreads ? (const void *)&jssm::batch_maps_kernel<1>
+                        : p.requests <= 4 * jssm::kMapsThreads ? (const void *)&jssm::batch_maps_kernel<4>
+                                                               : (const void *)&jssm::batch_maps_kernel<8>;
+        st = launch_early(k, dim3(ctas > 0 ? ctas : 1), jssm::kMapsThreads, 0, 1, args, stream);
+    } else {
+        st = launch_early((const void *)&jssm::batch_maps_requests_kernel, dim3(1),
+                          jssm::kMapsManyThreads, 0, 1, args, stream);
+        if (st == JAMBA_SSM_OK && ctas > 0)
+            st = launch_early((const void *)&jssm::batch_maps_tokens_kernel, dim3(ctas),
+                              jssm::kMapsThreads, 0, 1, args, stream);
+    }
     return st != JAMBA_SSM_OK ? st : finish_launch(stream, nullptr);
 }
 

@@ -15,7 +15,8 @@ import torch
 
 from . import _lib
 from ._lib import JambaSSMError
-from ._tensors import IO, check, cuda_device, launching, ptr, raw_stream, row_stride
+from ._tensors import (IO, check, cuda_device, empty_like, launching, ptr, raw_stream,
+                       row_stride)
 from ._tensors import workspace as _workspace
 
 __all__ = ["jamba_ssm_gated_scan", "jamba_ssm_gated_scan_ckpt", "jamba_ssm_gated_scan_ckpt_size",
@@ -93,9 +94,9 @@ def jamba_ssm_gated_scan(x, g, z=None, rate=None, bias=None, h0=None, out=None, 
     ws, ws_bytes = _workspace(workspace, dev)
     with launching(stream, dev):
         if out is None:
-            out = torch.empty(shape, dtype=io, device=dev)
+            out = empty_like(x, xs == 0)
         if h_final is None and return_final_state and state_indices is None:
-            h_final = torch.empty(state, dtype=_F32, device=dev)
+            h_final = x.new_empty(state, dtype=_F32) if h0 is None else empty_like(h0)
         p = _lib.GatedScanParams(_SCAN, batch, seqlen, d, IO[io], 0, ptr(x), ptr(g), ptr(z), xs,
                                  gs, zs, ptr(rate), ptr(bias), ptr(h0), ptr(out), ptr(h_final),
                                  ptr(cu_seqlens), rows, ptr(state_indices), ptr(initial_indices),
@@ -157,13 +158,13 @@ def jamba_ssm_gated_scan_bwd(x, g, dout, z=None, rate=None, bias=None, h0=None, 
     with launching(stream, dev):
         if workspace is None:
             need = L.jamba_ssm_gated_scan_bwd_workspace_size(batch, rows, d, ckpt is not None)
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            workspace = x.new_empty(need, dtype=torch.uint8)
         ws, ws_bytes = _workspace(workspace, dev)
-        dx, dg = (torch.empty(shape, dtype=io, device=dev) for _ in range(2))
-        dz = None if z is None else torch.empty(shape, dtype=io, device=dev)
-        drate = None if rate is None else torch.empty(d, dtype=_F32, device=dev)
-        dbias = None if bias is None else torch.empty(d, dtype=_F32, device=dev)
-        dh0 = torch.empty(batch, d, dtype=_F32, device=dev)
+        dx, dg = empty_like(dout), empty_like(dout)
+        dz = None if z is None else empty_like(dout)
+        drate = None if rate is None else empty_like(rate)
+        dbias = None if bias is None else empty_like(bias)
+        dh0 = x.new_empty((batch, d), dtype=_F32)
         p = _lib.GatedScanBwdParams(_BWD, batch, seqlen, d, IO[io], 0, ptr(x), ptr(g), ptr(z), xs,
                                     gs, zs, ptr(rate), ptr(bias), ptr(h0), ptr(dout),
                                     ptr(dh_final), ptr(dx), ptr(dg), ptr(dz), ptr(drate),
@@ -203,7 +204,7 @@ def jamba_ssm_gated_state_update(state, x, g, z=None, rate=None, bias=None, out=
     ws, ws_bytes = _workspace(workspace, dev)
     with launching(stream, dev):
         if out is None:
-            out = torch.empty(shape, dtype=io, device=dev)
+            out = empty_like(x, xs == 0)
         p = _lib.GatedStateUpdateParams(_UPDATE, batch, d, IO[io], 0, ptr(state), ptr(x), ptr(g),
                                         ptr(z), xs, gs, zs, ptr(rate), ptr(bias), ptr(out),
                                         ptr(state_indices), slots, ws, ws_bytes)

@@ -50,9 +50,9 @@ def jamba_ssm_i8_quant(x, q=None, scale=None, stream=None):
     check(scale, "scale", lead, _F32, dev)
     with launching(stream, dev):
         if q is None:
-            q = torch.empty((*lead, pitch), dtype=_I8, device=dev)
+            q = x.new_empty((*lead, pitch), dtype=_I8)
         if scale is None:
-            scale = torch.empty(lead, dtype=_F32, device=dev)
+            scale = x.new_empty(lead, dtype=_F32)
         p = _lib.I8QuantParams(_QUANT, rows, k, IO[x.dtype], 0, ptr(x), xs, ptr(q), ptr(scale))
         st = _lib.serve_lib().jamba_ssm_i8_quant(byref(p), raw_stream(dev))
     if st != _lib.OK:
@@ -86,7 +86,7 @@ def jamba_ssm_i8_proj(q, q_scale, w, w_scale, bias=None, out=None, out_dtype=tor
     check(out, "out", (*lead, n), out_dtype, dev)
     with launching(stream, dev):
         if out is None:
-            out = torch.empty((*lead, n), dtype=out_dtype, device=dev)
+            out = q.new_empty((*lead, n), dtype=out_dtype)
         p = _lib.I8ProjParams(_PROJ, lead.numel(), pitch, n, IO[out_dtype], 0, ptr(q),
                               ptr(q_scale), ptr(w), ptr(w_scale), ptr(bias), ptr(out),
                               int(timeout_cycles))
@@ -130,10 +130,12 @@ def jamba_ssm_batch_maps(new_lens, block_tables, free_blocks, request_slots, fre
     check(free_slots, "free_slots", free_slots.shape, _I32, dev)
     t = int(max_tokens)
     with launching(stream, dev):
-        # one buffer: slot_map first (its 8-byte elements), then the int32 maps
-        buf = torch.empty(4 * t + 3 * n + 5, dtype=_I32, device=dev)
-        slot_map = buf[:2 * t].view(_I64)
-        pos, req, cu, si, ii, counts = buf[2 * t:].split((t, t, n + 1, n, n, 4))
+        # one buffer, the per-token maps first, each of them from a multiple of 16 bytes on
+        r = -t % 4
+        buf = new_lens.new_empty(4 * (t + r) + 3 * n + 5)
+        slot_map, _, pos, _, req, _, cu, si, ii, counts = buf.split(
+            (2 * t, 2 * r, t, r, t, r, n + 1, n, n, 4))
+        slot_map = slot_map.view(_I64)
         p = _lib.BatchMapsParams(_MAPS, n, t, width, int(block_size), ptr(new_lens),
                                  ptr(ctx_lens), ptr(free_blocks), free_blocks.numel(),
                                  ptr(free_slots), free_slots.numel(), ptr(block_tables),
