@@ -110,8 +110,9 @@ template <int VEC> __device__ __forceinline__ Lane<VEC> lsigmoid(Lane<VEC> v) {
 // r = 1 / (p q) gives r q and r p.  The special-function pipe, at 4 lanes a
 // cycle and scheduler, is the scan's narrowest: this takes 3 of its operations
 // a pair instead of 4.  Where p q leaves the range (v0 + v1 below about -87) or
-// an input is a NaN, r is not above 0: `good` is cleared, and the caller does
-// the run again with lsigmoid.
+// an input is a NaN, r is not above 0: `good` is cleared, and the lane does its
+// run again with lsigmoid (each lane for itself: a result must not depend on
+// what the other lanes hold).
 __device__ __forceinline__ Lane2 lsigmoid_pair(Lane2 v, bool &good) {
     const Lane2 t = lmul(v, Lane2::of(-kLog2e));
     const Lane2 qp = ladd(Lane2{make_float2(ex2_mufu(t.v.y), ex2_mufu(t.v.x))}, Lane2::of(1.0f));
@@ -259,11 +260,17 @@ template <typename T, int VEC, int S, int Q, int CP> struct GatedFeed {
         }
         p += round;
     }
+    __device__ __forceinline__ void skip() { p += round; }
 };
 
 __device__ __forceinline__ Lane1 lshfl_up(Lane1 a, int by) { return {__shfl_up_sync(~0u, a.v, by)}; }
 __device__ __forceinline__ Lane2 lshfl_up(Lane2 a, int by) {
     return {make_float2(__shfl_up_sync(~0u, a.v.x, by), __shfl_up_sync(~0u, a.v.y, by))};
+}
+
+__device__ __forceinline__ Lane1 lshfl_down(Lane1 a, int by) { return {__shfl_down_sync(~0u, a.v, by)}; }
+__device__ __forceinline__ Lane2 lshfl_down(Lane2 a, int by) {
+    return {make_float2(__shfl_down_sync(~0u, a.v.x, by), __shfl_down_sync(~0u, a.v.y, by))};
 }
 
 // ------------------------------------------------------------------- the scan
@@ -410,7 +417,7 @@ __global__ void __launch_bounds__(kGatedThreads, 4) gated_scan_kernel(const Gate
                 h[i] = ph, P[i] = pp;
             }
         }
-        if (!__all_sync(~0u, good)) {
+        if (!good && on) {
             ph = zero, pp = one;
 #pragma unroll
             for (int i = 0; i < S; ++i) {
@@ -504,7 +511,7 @@ __global__ void __launch_bounds__(kGatedThreads, 4) gated_scan_kernel(const Gate
                 o += a.d;
             }
         }
-        if (!__all_sync(~0u, good)) {
+        if (!good && on) {
             T *o = op;
 #pragma unroll
             for (int i = 0; i < S; ++i) {
@@ -529,70 +536,6 @@ __global__ void __launch_bounds__(kGatedThreads, 4) gated_scan_kernel(const Gate
 #pragma unroll
         for (int v = 0; v < VEC; ++v) a.h_final[out_row * a.d + c + v] = carry.get(v);
     }
-}
-
-// Backward: per 64-step block, last block first, the states again from the
-// block's checkpoint, then the gradients in reverse.
-template <typename T> __global__ void gated_scan_bwd_kernel(const GatedArgs a) {
-    const int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;
-    const int b = static_cast<int>(i / a.d), c = static_cast<int>(i % a.d);
-    if (b >= a.batch) return;
-    int64_t row0, len;
-    gated_rows(a, b, row0, len);
-    const float rate = a.rate ? a.rate[c] : 1.0f, bias = a.bias ? a.bias[c] : 0.0f;
-    const T *x = static_cast<const T *>(a.x), *g = static_cast<const T *>(a.g),
-            *z = static_cast<const T *>(a.z), *dout = static_cast<const T *>(a.dout);
-    T *dx = static_cast<T *>(a.dx), *dg = static_cast<T *>(a.dg), *dz = static_cast<T *>(a.dz);
-    float carry = a.dh_final ? a.dh_final[int64_t(b) * a.d + c] : 0.0f;
-    float drate = 0.0f, dbias = 0.0f;
-    float hp[kGatedCkpt];
-    for (int64_t k = (len + kGatedCkpt - 1) / kGatedCkpt - 1; k >= 0; --k) {
-        const int64_t t0 = k * kGatedCkpt;
-        const int n = static_cast<int>(min(int64_t(kGatedCkpt), len - t0));
-        float h = a.ckpt[(row0 / kGatedCkpt + b + k) * a.d + c];
-        for (int t = 0; t < n; ++t) {
-            const int64_t r = row0 + t0 + t;
-            hp[t] = h;
-            h = fmaf(rate * sigmoid_f32(to_f32(g[r * a.gs + c]) + bias), to_f32(x[r * a.xs + c]) - h, h);
-        }
-        for (int t = n - 1; t >= 0; --t) {
-            const int64_t r = row0 + t0 + t;
-            const float s = sigmoid_f32(to_f32(g[r * a.gs + c]) + bias), u = rate * s;
-            const float xv = to_f32(x[r * a.xs + c]), dv = to_f32(dout[r * a.d + c]);
-            float gh = carry;
-            if (z) {
-                const float zv = to_f32(z[r * a.zs + c]), sz = sigmoid_f32(zv);
-                const float ht = fmaf(u, xv - hp[t], hp[t]);
-                gh += dv * (zv * sz);
-                dz[r * a.d + c] = from_f32<T>(dv * ht * (sz * fmaf(zv, 1.0f - sz, 1.0f)));
-            } else {
-                gh += dv;
-            }
-            const float du = gh * (xv - hp[t]);
-            const float dgv = du * u * (1.0f - s);
-            dx[r * a.d + c] = from_f32<T>(u * gh);
-            dg[r * a.d + c] = from_f32<T>(dgv);
-            drate += du * s;
-            dbias += dgv;
-            carry = fmaf(-u, gh, gh);
-        }
-    }
-    if (a.dh0) a.dh0[int64_t(b) * a.d + c] = carry;
-    a.partial[int64_t(2 * b) * a.d + c] = drate;
-    a.partial[int64_t(2 * b + 1) * a.d + c] = dbias;
-}
-
-// drate and dbias: the sequences' partial sums added in their order.
-__global__ void gated_reduce_kernel(const float *partial, float *drate, float *dbias, int batch, int d) {
-    const int c = blockIdx.x * blockDim.x + threadIdx.x;
-    if (c >= d) return;
-    float r = 0.0f, s = 0.0f;
-    for (int b = 0; b < batch; ++b) {
-        r += partial[int64_t(2 * b) * d + c];
-        s += partial[int64_t(2 * b + 1) * d + c];
-    }
-    if (drate) drate[c] = r;
-    if (dbias) dbias[c] = s;
 }
 
 }  // namespace jssm

@@ -5,6 +5,7 @@
 #include "jamba_ssm_gated.h"
 
 #include "gated_scan.cuh"
+#include "gated_scan_bwd.cuh"
 #include "gated_update.cuh"
 #include "host_utils.h"
 
@@ -121,7 +122,7 @@ struct Kernel {
 // Raises a kernel's dynamic shared-memory limit, once per kernel and device.
 cudaError_t raise_smem(const Kernel &k, int dev) {
     static std::mutex mutex;
-    static const void *done[kMaxDevices][64];
+    static const void *done[kMaxDevices][128];
     std::lock_guard<std::mutex> lock(mutex);
     for (const void *&slot : done[dev]) {
         if (slot == k.fn) return cudaSuccess;
@@ -182,6 +183,36 @@ jamba_ssm_status launch_scan(jssm::GatedArgs &a, int32_t dtype, const DeviceInfo
                      : cp == 16 ? scan_kernel<Bf, 2, 16>(gate, q, cs)
                      : cp == 4  ? scan_kernel<Bf, 2, 4>(gate, q, cs)
                                 : scan_kernel<Bf, 1, 2>(gate, q, cs);
+    return launch_clusters(k, cut.units, cs, args, dev, stream);
+}
+
+template <typename T, int VEC, int CP, int Q, bool CL> Kernel bwd_kernel_q(bool gate) {
+    return gate ? Kernel{(const void *)&jssm::gated_scan_bwd_kernel<T, VEC, true, Q, CP, CL>,
+                         jssm::kGatedBwdThreads, jssm::GatedBwdCfg<true>::kSmemBytes}
+                : Kernel{(const void *)&jssm::gated_scan_bwd_kernel<T, VEC, false, Q, CP, CL>,
+                         jssm::kGatedBwdThreads, jssm::GatedBwdCfg<false>::kSmemBytes};
+}
+template <typename T, int VEC, int CP, bool CL> Kernel bwd_kernel_c(bool gate, int q) {
+    return q == 1 ? bwd_kernel_q<T, VEC, CP, 1, CL>(gate)
+         : q == 2 ? bwd_kernel_q<T, VEC, CP, 2, CL>(gate)
+                  : bwd_kernel_q<T, VEC, CP, 4, CL>(gate);
+}
+template <typename T, int VEC, int CP> Kernel bwd_kernel(bool gate, int q, int cs) {
+    return cs > 1 ? bwd_kernel_c<T, VEC, CP, true>(gate, q) : bwd_kernel_c<T, VEC, CP, false>(gate, q);
+}
+
+jamba_ssm_status launch_bwd(jssm::GatedArgs &a, int32_t dtype, const DeviceInfo *dev, void *stream) {
+    const int cp = copy_bytes(a, dtype);
+    const bool bf = dtype == JAMBA_SSM_BF16, gate = a.z != nullptr;
+    const int width = bf && cp >= 4 ? 64 : 32;
+    Cut cut = choose_cut(a.batch, a.cu ? a.total / a.batch : a.seqlen, dev->sms,
+                         [&](int q) { return int64_t(a.d + width / q - 1) / (width / q); });
+    int q = cut.q, cs = cut.cs;
+    void *args[] = {&a, &cs};
+    const Kernel k = !bf ? (cp == 16 ? bwd_kernel<float, 1, 16>(gate, q, cs) : bwd_kernel<float, 1, 4>(gate, q, cs))
+                     : cp == 16 ? bwd_kernel<Bf, 2, 16>(gate, q, cs)
+                     : cp == 4  ? bwd_kernel<Bf, 2, 4>(gate, q, cs)
+                                : bwd_kernel<Bf, 1, 2>(gate, q, cs);
     return launch_clusters(k, cut.units, cs, args, dev, stream);
 }
 
@@ -298,23 +329,17 @@ jamba_ssm_gated_scan_bwd(const jamba_ssm_gated_scan_bwd_params *pin, void *strea
     a.dh0 = p.dh0;
     a.partial = static_cast<float *>(p.workspace);
     a.ckpt = const_cast<float *>(p.ckpt);
-    void *args[] = {&a};
     if (p.batch > 0) {
         if (!a.ckpt) {
             a.ckpt = a.partial + partial_bytes(p.batch, p.d_inner) / 4;
             if ((st = launch_scan(a, p.io_dtype, dev, stream)) != JAMBA_SSM_OK) return st;
         }
-        const int64_t grid = (p.batch * p.d_inner + 127) / 128;
-        if (grid > 0x7fffffff) return JAMBA_SSM_ERR_UNSUPPORTED;
-        st = launch(p.io_dtype == JAMBA_SSM_BF16
-                        ? (const void *)&jssm::gated_scan_bwd_kernel<__nv_bfloat16>
-                        : (const void *)&jssm::gated_scan_bwd_kernel<float>,
-                    static_cast<unsigned>(grid), 128, args, stream);
-        if (st != JAMBA_SSM_OK) return st;
+        if (p.batch == 1) a.partial = nullptr;  // one sequence's sums are the sums
+        if ((st = launch_bwd(a, p.io_dtype, dev, stream)) != JAMBA_SSM_OK) return st;
     }
-    if (a.drate || a.dbias) {
-        void *rargs[] = {&a.partial, &a.drate, &a.dbias, &a.batch, &a.d};
-        st = launch((const void *)&jssm::gated_reduce_kernel, unsigned((a.d + 127) / 128), 128, rargs, stream);
+    if ((a.drate || a.dbias) && p.batch != 1) {
+        void *args[] = {&a.partial, &a.drate, &a.dbias, &a.batch, &a.d};
+        st = launch((const void *)&jssm::gated_reduce_kernel, unsigned((a.d + 127) / 128), 128, args, stream);
         if (st != JAMBA_SSM_OK) return st;
     }
     return finish_launch(stream, nullptr);

@@ -305,6 +305,28 @@ def test_backward_of_nothing():
     assert (got["drate"] == 0).all() and got["dh0"].shape == (0, 8)
 
 
+def test_neighbours_and_what_memory_held_change_no_bits():
+    """A channel pair's results are its own inputs' alone: not those of the other
+    lanes of its warp, which may have to do their rows again, nor what shared
+    memory held for lanes past the width."""
+    x, g, z, rate, bias = _inputs((1, 1100, 34), BF, 8)
+    dout = torch.randn(x.shape, device=x.device).to(BF)
+    one, _ = jamba_ssm_gated_scan(x, g, z=z, rate=rate, bias=bias)
+    back = jamba_ssm_gated_scan_bwd(x, g, dout, z=z, rate=rate, bias=bias)
+    dirty = torch.full((64, 512, 512), float("nan"), dtype=BF, device=x.device)
+    g2 = g.clone()
+    g2[0, ::7, 6:8] = -80.0  # one pair whose exponentials' product overflows
+    g2[0, 5, 20] = float("nan")
+    keep = [c for c in range(34) if c not in (6, 7, 20, 21)]
+    for _ in range(4):
+        jamba_ssm_gated_scan(dirty, dirty)  # leaves NaN behind
+        out, _ = jamba_ssm_gated_scan(x, g2, z=z, rate=rate, bias=bias)
+        assert torch.equal(out[..., keep], one[..., keep])
+        got = jamba_ssm_gated_scan_bwd(x, g2, dout, z=z, rate=rate, bias=bias)
+        for k, v in got.items():
+            assert torch.equal(v[..., keep], back[k][..., keep]), k
+
+
 def test_gradients_of_runs_are_the_same_bits():
     x, g, z, rate, bias = _inputs((3, 700, 160), BF, 12)
     dout = torch.randn(x.shape, device=x.device).to(BF)
