@@ -8,7 +8,7 @@
 // c runs backwards through the sequence as the state runs forwards: a run of
 // rows maps the c behind it to P c + R with the same P = prod(1 - u), and runs
 // compose.  So the kernel is the scan's with the order reversed: a lane takes a
-// run of 8 rows, a warp Q runs, a CTA's 8 warps a chunk of 64 Q rows, a cluster
+// run of 16 rows, a warp Q runs, a CTA's 4 warps a chunk of 64 Q rows, a cluster
 // consecutive chunks, from the sequence's end to its start.  The states that du
 // and dz need come from the forward's checkpoints, one for every 64 rows, so
 // they need no exchange beyond the 64 rows' own runs.  One barrier a round
@@ -21,10 +21,11 @@
 #pragma once
 
 #include "gated_scan.cuh"
+#include "launch_order.cuh"
 
 namespace jssm {
 
-constexpr int kGatedBwdWarps = 8, kGatedBwdRun = 8, kGatedBwdThreads = 32 * kGatedBwdWarps;
+constexpr int kGatedBwdWarps = 4, kGatedBwdRun = 16, kGatedBwdThreads = 32 * kGatedBwdWarps;
 static_assert(kGatedBwdWarps * kGatedBwdRun == kGatedCkpt, "W / Q warps take a checkpoint's rows");
 
 template <bool GATE> struct GatedBwdCfg {
@@ -35,7 +36,7 @@ template <bool GATE> struct GatedBwdCfg {
 };
 
 template <typename T, int VEC, bool GATE, int Q, int CP, bool CLUSTER>
-__global__ void __launch_bounds__(kGatedBwdThreads, 2) gated_scan_bwd_kernel(const GatedArgs a, int cs) {
+__global__ void __launch_bounds__(kGatedBwdThreads, 3) gated_scan_bwd_kernel(const GatedArgs a, int cs) {
     using Raw = GatedRaw<T, VEC>;
     using R = typename Raw::type;
     using C = GatedBwdCfg<GATE>;
@@ -96,7 +97,7 @@ __global__ void __launch_bounds__(kGatedBwdThreads, 2) gated_scan_bwd_kernel(con
         rate.set(v, on && a.rate ? a.rate[c + v] : 1.0f);
         bias.set(v, on && a.bias ? a.bias[c + v] : 0.0f);
     }
-    const L one = L::of(1.0f), zero = L::of(0.0f), minus = L::of(-1.0f);
+    const L one = L::of(1.0f), zero = L::of(0.0f), nrate = lmul(rate, L::of(-1.0f));
     L drate = zero, dbias = zero;
     const float *ck = a.ckpt + (row0 / kGatedCkpt + b) * a.d + c;  // the sequence's first entry
     auto checkpoint = [&](int at) {  // the state before the 64 rows around row `at`
@@ -112,51 +113,48 @@ __global__ void __launch_bounds__(kGatedBwdThreads, 2) gated_scan_bwd_kernel(con
         const int par = k & 1;
         const bool full = len - t >= S * Q;
         const int n = min(len - t - run * S, S);  // rows of this lane's run
-        const uint8_t *st = mine + par * C::kStageBytes;
+        uint8_t *st = mine + par * C::kStageBytes;
         const R *gr = reinterpret_cast<const R *>(st) + lane;
         const R *xr = reinterpret_cast<const R *>(st + C::kArrayBytes) + lane;
         const R *dr = reinterpret_cast<const R *>(st + 2 * C::kArrayBytes) + lane;
+        // x - h_{t-1} takes the place of g and x once they have been used
+        float *d0 = reinterpret_cast<float *>(st) + lane;
+        float *d1 = reinterpret_cast<float *>(st + C::kArrayBytes) + lane;
         const R *zr = reinterpret_cast<const R *>(st + 3 * C::kArrayBytes) + lane;
         const L next_block = checkpoint(t - stride);
         cp_async_wait<1>();
         __syncwarp();
-        // forwards: the run's map of the state; the sigmoids and dL/d(h before its gate)
-        L s[S], dy[S], sz[GATE ? S : 1], P = one, hb = zero;
+        // the run's maps: of the state, P h + hb, and of the gradient, P c + rb.  The
+        // latter is a sum forwards too: row i's dy reaches the rows before the run
+        // through the product of (1 - u) up to and with its own.
+        L s[S], dy[S], P = one, hb = zero, rb = zero;  // dy holds sigmoid(z) until z has been used
         auto ahead = [&](int i) {
-            const L nu = lmul(lmul(s[i], rate), minus);
+            const L nu = lmul(s[i], nrate);
             hb = lfma(nu, lsub(hb, Raw::get(xr[i * 32])), hb);
             P = lfma(nu, P, P);
-            dy[i] = Raw::get(dr[i * 32]);
-            if (GATE) dy[i] = lmul(dy[i], lmul(Raw::get(zr[i * 32]), sz[i]));
+            L d = Raw::get(dr[i * 32]);
+            if (GATE) d = lmul(d, lmul(Raw::get(zr[i * 32]), dy[i]));
+            rb = lfma(P, d, rb);
         };
         bool good = full;
         if (full) {
 #pragma unroll
             for (int i = 0; i < S; ++i) {
                 s[i] = lsigmoid_pair(ladd(Raw::get(gr[i * 32]), bias), good);
-                if (GATE) sz[i] = lsigmoid_pair(Raw::get(zr[i * 32]), good);
+                if (GATE) dy[i] = lsigmoid_pair(Raw::get(zr[i * 32]), good);
                 ahead(i);
             }
         }
         if (!good && on) {
-            P = one, hb = zero;
+            P = one, hb = rb = zero;
 #pragma unroll
             for (int i = 0; i < S; ++i) {
-                s[i] = dy[i] = zero;
-                if (GATE) sz[i] = zero;
                 if (i < n) {
                     s[i] = lsigmoid(ladd(Raw::get(gr[i * 32]), bias));
-                    if (GATE) sz[i] = lsigmoid(Raw::get(zr[i * 32]));
+                    if (GATE) dy[i] = lsigmoid(Raw::get(zr[i * 32]));
                     ahead(i);
                 }
             }
-        }
-        // backwards: what the run hands to the rows before it, from nothing behind it
-        L rb = zero;
-#pragma unroll
-        for (int i = S - 1; i >= 0; --i) {
-            const L gh = ladd(dy[i], rb);
-            rb = lfma(lmul(lmul(s[i], rate), minus), gh, gh);
         }
         // the warp's runs before and behind this one; P and both totals over the warp
         L bp = one, bb = zero, ap = one, ab = zero, wp = P, wb = hb, wr = rb;
@@ -192,13 +190,13 @@ __global__ void __launch_bounds__(kGatedBwdThreads, 2) gated_scan_bwd_kernel(con
         // the state before this run: the block's checkpoint through the runs between
         L h = block;
         const int w0 = warp / kBlockWarps * kBlockWarps;
+        Map maps[W];
+        L backs[W];
 #pragma unroll
-        for (int w = 0; w < kBlockWarps - 1; ++w) {
-            if (w0 + w < warp) {
-                const Map r = runs[par][w0 + w][col];
-                h = lfma(r.P(), h, r.b());
-            }
-        }
+        for (int w = 0; w < W; ++w) maps[w] = runs[par][w][col], backs[w] = back[par][w][col];
+#pragma unroll
+        for (int w = 0; w < W - 1; ++w)
+            if (w >= w0 && w < warp) h = lfma(maps[w].P(), h, maps[w].b());
         h = lfma(bp, h, bb);
         // c behind this warp's rows
         L cb;
@@ -208,13 +206,12 @@ __global__ void __launch_bounds__(kGatedBwdThreads, 2) gated_scan_bwd_kernel(con
 #pragma unroll
             for (int w = W - 1; w > 0; --w) {
                 if (w > warp) {
-                    const L p = runs[par][w][col].P();
-                    cb = lfma(p, cb, back[par][w][col]);
-                    mp = lmul(p, mp);
+                    cb = lfma(maps[w].P(), cb, backs[w]);
+                    mp = lmul(maps[w].P(), mp);
                 }
             }
             if (warp == 0 && run == 0) {  // the chunk's map to every CTA of the cluster
-                const L p = runs[par][0][col].P();
+                const L p = maps[0].P();
                 const Map m = Map::of(lmul(p, mp), lfma(p, cb, wr));
                 const uint32_t at = smem_u32(&chunks[par][rank][col]);
 #pragma unroll
@@ -239,25 +236,28 @@ __global__ void __launch_bounds__(kGatedBwdThreads, 2) gated_scan_bwd_kernel(con
             cb = carry;
 #pragma unroll
             for (int w = W - 1; w > 0; --w)
-                if (w > warp) cb = lfma(runs[par][w][col].P(), cb, back[par][w][col]);
-            if (warp == 0 && run == 0) last[par ^ 1][col] = lfma(runs[par][0][col].P(), cb, wr);
+                if (w > warp) cb = lfma(maps[w].P(), cb, backs[w]);
+            if (warp == 0 && run == 0) last[par ^ 1][col] = lfma(maps[0].P(), cb, wr);
         }
         cb = lfma(ap, cb, ab);  // behind this run
         // forwards again from the true state: dz, and x - h_{t-1}
-        L diff[S];
         T *dz = static_cast<T *>(a.dz) + o0;
 #pragma unroll
         for (int i = 0; i < S; ++i) {
             if (full || i < n) {
-                diff[i] = lsub(Raw::get(xr[i * 32]), h);
-                h = lfma(lmul(s[i], rate), diff[i], h);
+                const L diff = lsub(Raw::get(xr[i * 32]), h);
+                h = lfma(lmul(s[i], rate), diff, h);
+                L d = Raw::get(dr[i * 32]);
                 if (GATE) {
                     // silu' = sz + z sz (1 - sz)
-                    const L zs = lmul(Raw::get(zr[i * 32]), sz[i]);
-                    const L slope = lfma(lsub(one, sz[i]), zs, sz[i]);
-                    const L v = lmul(lmul(Raw::get(dr[i * 32]), h), slope);
-                    if (on) *reinterpret_cast<R *>(dz) = Raw::put(v);
+                    const L sz = dy[i], zs = lmul(Raw::get(zr[i * 32]), sz);
+                    const L slope = lfma(lsub(one, sz), zs, sz);
+                    if (on) *reinterpret_cast<R *>(dz) = Raw::put(lmul(lmul(d, h), slope));
+                    d = lmul(d, zs);
                 }
+                dy[i] = d;
+                d0[i * 32] = diff.get(0);
+                if constexpr (VEC == 2) d1[i * 32] = diff.get(1);
             }
             if (GATE) dz += a.d;
         }
@@ -268,10 +268,14 @@ __global__ void __launch_bounds__(kGatedBwdThreads, 2) gated_scan_bwd_kernel(con
         for (int i = S - 1; i >= 0; --i) {
             dx -= a.d, dg -= a.d;
             if (full || i < n) {
-                const L gh = ladd(dy[i], cb), u = lmul(s[i], rate);
-                const L x = lmul(u, gh), du = lmul(gh, diff[i]);
-                const L g = lmul(lmul(du, u), lsub(one, s[i]));
-                sr = lfma(du, s[i], sr);
+                L diff;
+                diff.set(0, d0[i * 32]);
+                if constexpr (VEC == 2) diff.set(1, d1[i * 32]);
+                const L gh = ladd(dy[i], cb);
+                const L x = lmul(lmul(s[i], rate), gh), du = lmul(gh, diff);
+                const L dus = lmul(du, s[i]);
+                const L g = lmul(lmul(dus, rate), lsub(one, s[i]));
+                sr = ladd(sr, dus);
                 sg = ladd(sg, g);
                 cb = lsub(gh, x);
                 if (on) {
@@ -343,6 +347,8 @@ __global__ void __launch_bounds__(kGatedBwdThreads, 2) gated_scan_bwd_kernel(con
 // drate and dbias: the sequences' sums added in their order.
 __global__ void gated_reduce_kernel(const float *partial, float *drate, float *dbias, int batch, int d) {
     const int c = blockIdx.x * blockDim.x + threadIdx.x;
+    after_earlier_work();
+    let_next_begin();
     if (c >= d) return;
     double r = 0.0, s = 0.0;
     for (int b = 0; b < batch; ++b) {

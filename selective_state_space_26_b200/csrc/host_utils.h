@@ -134,27 +134,38 @@ inline jamba_ssm_status finish_launch(void *stream, void *workspace) {
     return sync_check ? read_status(workspace, stream) : JAMBA_SSM_OK;
 }
 
-// Launches `k`, its clusters `cs` CTAs along x, and lets it begin while the work
-// before it in the stream ends: such a kernel touches no memory before its
+// Launches `k`, its clusters `cs` CTAs along x.  `early`: it may begin while the
+// work before it in the stream ends; such a kernel touches no memory before its
 // griddepcontrol.wait (jssm::after_earlier_work), so only its own start -- the
 // launch itself, barriers, TMEM -- overlaps.
-inline jamba_ssm_status launch_early(const void *k, dim3 grid, unsigned threads, size_t smem, int cs,
-                                     void **args, void *stream) {
+inline jamba_ssm_status launch(const void *k, dim3 grid, unsigned threads, size_t smem, int cs, bool early,
+                               void **args, void *stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = static_cast<cudaStream_t>(stream);
     cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = static_cast<unsigned>(cs);
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    unsigned n = 0;
+    if (early) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    if (cs > 1) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = static_cast<unsigned>(cs);
+        attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
+        ++n;
+    }
     cfg.attrs = attr;
-    cfg.numAttrs = cs > 1 ? 2 : 1;
+    cfg.numAttrs = n;
     const cudaError_t e = cudaLaunchKernelExC(&cfg, k, args);
     return e == cudaSuccess ? JAMBA_SSM_OK : cuda_fail(e);
+}
+
+inline jamba_ssm_status launch_early(const void *k, dim3 grid, unsigned threads, size_t smem, int cs,
+                                     void **args, void *stream) {
+    return launch(k, grid, threads, smem, cs, true, args, stream);
 }
 
 }  // namespace jssm_host

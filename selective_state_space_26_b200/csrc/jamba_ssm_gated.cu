@@ -63,12 +63,6 @@ template <typename P> void fill_common(const P &p, int64_t rows, jssm::GatedArgs
     a->batch = static_cast<int>(p.batch);
 }
 
-jamba_ssm_status launch(const void *k, unsigned grid, unsigned threads, void **args, void *stream) {
-    cudaError_t e = cudaLaunchKernel(k, dim3(grid), dim3(threads), args, 0,
-                                     static_cast<cudaStream_t>(stream));
-    return e == cudaSuccess ? JAMBA_SSM_OK : cuda_fail(e);
-}
-
 // How the rows can be read: bytes of one copy, the largest of 16, 4 and 2 that
 // divides the width, the strides and every pointer.
 int copy_bytes(const jssm::GatedArgs &a, int32_t dtype) {
@@ -97,19 +91,21 @@ struct Cut {
 //   13 x 4096 rows x 2048:     q 1 158, q 2 165, in clusters of 8 from 247.
 // So: one CTA to a tile where 2 (q = 1) or 1.5 (q = 2) of them come to an SM;
 // else clusters, whose barrier costs about a round's time and is hidden by the
-// other CTAs of an SM, up to 4 of them; q = 4 where that leaves under 2.
-template <typename Tiles> Cut choose_cut(int64_t batch, int64_t len, int sms, Tiles tiles) {
+// other CTAs of an SM, up to the per_sm that fit one (4 of the scan's, 3 of the
+// backward's); q = 4 where that leaves under 1.5.  The backward alike: 1024
+// channels, 4096 rows, both passes: q 2 in clusters of 8 39, q 4 of 4 44, of 8 50.
+template <typename Tiles> Cut choose_cut(int64_t batch, int64_t len, int sms, int per_sm, Tiles tiles) {
     auto clusters = [&](int q) {
         const int64_t units = batch * tiles(q), rows = int64_t(jssm::kGatedCkpt) * q;
         int cs = 1;
-        while (cs < jssm::kGatedMaxCluster && cs * 2 <= (len + rows - 1) / rows && units * cs * 2 <= 4 * sms)
+        while (cs < jssm::kGatedMaxCluster && cs * 2 <= (len + rows - 1) / rows && units * cs * 2 <= per_sm * sms)
             cs *= 2;
         return Cut{q, cs, units};
     };
     if (batch * tiles(1) >= 2 * sms) return {1, 1, batch * tiles(1)};
     if (batch * tiles(2) * 2 >= 3 * sms) return {2, 1, batch * tiles(2)};
     const Cut two = clusters(2);
-    return two.units * two.cs < 2 * sms ? clusters(4) : two;
+    return two.units * two.cs * 2 < 3 * sms ? clusters(4) : two;
 }
 
 using Bf = __nv_bfloat16;
@@ -139,21 +135,12 @@ cudaError_t raise_smem(const Kernel &k, int dev) {
 jamba_ssm_status launch_clusters(const Kernel &k, int64_t units, int cs, void **args,
                                  const DeviceInfo *dev, void *stream) {
     if (units * cs > 0x7fffffff) return JAMBA_SSM_ERR_UNSUPPORTED;
-    cudaError_t e = raise_smem(k, dev->id);
+    const cudaError_t e = raise_smem(k, dev->id);
     if (e != cudaSuccess) return cuda_fail(e);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(units * cs));
-    cfg.blockDim = dim3(k.threads);
-    cfg.dynamicSmemBytes = k.smem;
-    cfg.stream = static_cast<cudaStream_t>(stream);
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(cs);
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = cs > 1 ? 1 : 0;
-    e = cudaLaunchKernelExC(&cfg, k.fn, args);
-    return e == cudaSuccess ? JAMBA_SSM_OK : cuda_fail(e);
+    // not early: CTAs that wait beside the kernel before them take the free SMs'
+    // room first, and the cut's even share of the device is lost (220 us for 189)
+    return launch(k.fn, dim3(static_cast<unsigned>(units * cs)), unsigned(k.threads), k.smem, cs, false,
+                  args, stream);
 }
 
 template <typename T, int VEC, int CP, int Q, bool CL> Kernel scan_kernel_q(bool gate) {
@@ -175,7 +162,7 @@ jamba_ssm_status launch_scan(jssm::GatedArgs &a, int32_t dtype, const DeviceInfo
     const int cp = copy_bytes(a, dtype);
     const bool bf = dtype == JAMBA_SSM_BF16, gate = a.z != nullptr;
     const int width = bf && cp >= 4 ? 64 : 32;  // channels of a warp's row
-    const Cut cut = choose_cut(a.batch, a.cu ? a.total / a.batch : a.seqlen, dev->sms,
+    const Cut cut = choose_cut(a.batch, a.cu ? a.total / a.batch : a.seqlen, dev->sms, 4,
                                [&](int q) { return int64_t(a.d + width / q - 1) / (width / q); });
     int q = cut.q, cs = cut.cs;
     void *args[] = {&a, &cs};
@@ -205,8 +192,8 @@ jamba_ssm_status launch_bwd(jssm::GatedArgs &a, int32_t dtype, const DeviceInfo 
     const int cp = copy_bytes(a, dtype);
     const bool bf = dtype == JAMBA_SSM_BF16, gate = a.z != nullptr;
     const int width = bf && cp >= 4 ? 64 : 32;
-    Cut cut = choose_cut(a.batch, a.cu ? a.total / a.batch : a.seqlen, dev->sms,
-                         [&](int q) { return int64_t(a.d + width / q - 1) / (width / q); });
+    const Cut cut = choose_cut(a.batch, a.cu ? a.total / a.batch : a.seqlen, dev->sms, 3,
+                               [&](int q) { return int64_t(a.d + width / q - 1) / (width / q); });
     int q = cut.q, cs = cut.cs;
     void *args[] = {&a, &cs};
     const Kernel k = !bf ? (cp == 16 ? bwd_kernel<float, 1, 16>(gate, q, cs) : bwd_kernel<float, 1, 4>(gate, q, cs))
@@ -339,7 +326,8 @@ jamba_ssm_gated_scan_bwd(const jamba_ssm_gated_scan_bwd_params *pin, void *strea
     }
     if ((a.drate || a.dbias) && p.batch != 1) {
         void *args[] = {&a.partial, &a.drate, &a.dbias, &a.batch, &a.d};
-        st = launch((const void *)&jssm::gated_reduce_kernel, unsigned((a.d + 127) / 128), 128, args, stream);
+        st = launch_early((const void *)&jssm::gated_reduce_kernel, dim3(unsigned((a.d + 127) / 128)), 128, 0, 1,
+                          args, stream);
         if (st != JAMBA_SSM_OK) return st;
     }
     return finish_launch(stream, nullptr);
