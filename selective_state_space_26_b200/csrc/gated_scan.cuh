@@ -101,7 +101,6 @@ __device__ __forceinline__ Lane2 lsub(Lane2 a, Lane2 b) {
 }
 __device__ __forceinline__ Lane2 lex2(Lane2 a) { return {make_float2(ex2_mufu(a.v.x), ex2_mufu(a.v.y))}; }
 __device__ __forceinline__ Lane2 lrcp(Lane2 a) { return {make_float2(rcp_mufu(a.v.x), rcp_mufu(a.v.y))}; }
-// 1 / sigmoid(v) - 1 = e^-v, and sigmoid from it
 template <int VEC> __device__ __forceinline__ Lane<VEC> lsigmoid(Lane<VEC> v) {
     return lrcp(ladd(lex2(lmul(v, Lane<VEC>::of(-kLog2e))), Lane<VEC>::of(1.0f)));
 }
@@ -187,6 +186,31 @@ __device__ __forceinline__ void st_cluster(uint32_t saddr, uint32_t rank, RunMap
     asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(a), "f"(m.v.x), "f"(m.v.y),
                  "f"(m.v.z), "f"(m.v.w)
                  : "memory");
+}
+
+// The sequence that a cluster takes.  Clusters start in the order of their
+// number, so of packed sequences the longest goes first (of equal ones the
+// first), or a long one among the last would run on alone.  Up to as many
+// sequences as threads; more come in their order.  `order`: THREADS + 1 ints.
+template <int THREADS> __device__ __forceinline__ int gated_sequence(const GatedArgs &a, int nth, int *order) {
+    if (!a.cu || a.batch > THREADS || a.batch < 2) return nth;
+    int len = 0;
+    if (threadIdx.x < a.batch) {
+        int64_t row0, len64;
+        gated_rows(a, threadIdx.x, row0, len64);
+        order[threadIdx.x] = len = static_cast<int>(len64);
+    }
+    __syncthreads();
+    if (threadIdx.x < a.batch) {
+        int before = 0;
+        for (int j = 0; j < a.batch; ++j) {
+            const int l = order[j];
+            before += l > len || (l == len && j < int(threadIdx.x));
+        }
+        if (before == nth) order[THREADS] = threadIdx.x;
+    }
+    __syncthreads();
+    return order[THREADS];
 }
 
 // ------------------------------------------------------------------- staging
@@ -332,7 +356,8 @@ __global__ void __launch_bounds__(kGatedThreads, 4) gated_scan_kernel(const Gate
     const int rank = CLUSTER ? static_cast<int>(cluster_rank()) : 0;
     const int tiles = (a.d + LPR * VEC - 1) / (LPR * VEC);
     const int64_t unit = blockIdx.x / cs;
-    const int b = static_cast<int>(unit / tiles);
+    __shared__ int order[kGatedThreads + 1];
+    const int b = gated_sequence<kGatedThreads>(a, static_cast<int>(unit / tiles), order);
     const int c0 = static_cast<int>(unit % tiles) * LPR * VEC, c = c0 + col * VEC;
     const bool on = c < a.d;
 

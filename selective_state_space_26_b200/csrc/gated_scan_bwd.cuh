@@ -56,7 +56,8 @@ __global__ void __launch_bounds__(kGatedBwdThreads, 3) gated_scan_bwd_kernel(con
     const int rank = CLUSTER ? static_cast<int>(cluster_rank()) : 0;
     const int tiles = (a.d + LPR * VEC - 1) / (LPR * VEC);
     const int64_t unit = blockIdx.x / cs;
-    const int b = static_cast<int>(unit / tiles);
+    __shared__ int order[kGatedBwdThreads + 1];
+    const int b = gated_sequence<kGatedBwdThreads>(a, static_cast<int>(unit / tiles), order);
     const int c0 = static_cast<int>(unit % tiles) * LPR * VEC, c = c0 + col * VEC;
     const bool on = c < a.d;
 

@@ -81,8 +81,7 @@ struct Cut {
     int64_t units;  // clusters
 };
 
-// Of a scan over `batch` sequences of about `len` rows of `tiles(q)` channel
-// tiles.  A CTA of q = 1 reads 128 bytes of a row and takes 64 rows a round;
+// Of a pass over sequences of tiles(q) channel tiles each.  A CTA of q = 1 reads 128 bytes of a row and takes 64 rows a round;
 // q = 2 and 4 halve and quarter the width for two and four times the rows.
 // Measured on 148 SMs (bf16 with z, us):
 //   8192 channels, 4096 rows:  q 1 89, q 2 59, q 4 72, q 2 in clusters of 2 68;
@@ -94,16 +93,36 @@ struct Cut {
 // other CTAs of an SM, up to the per_sm that fit one (4 of the scan's, 3 of the
 // backward's); q = 4 where that leaves under 1.5.  The backward alike: 1024
 // channels, 4096 rows, both passes: q 2 in clusters of 8 39, q 4 of 4 44, of 8 50.
-template <typename Tiles> Cut choose_cut(int64_t batch, int64_t len, int sms, int per_sm, Tiles tiles) {
+// Packed sequences are ragged: the longest, taken as three times the mean, may
+// run on alone, so q goes up until its rounds take no longer than moving all
+// the bytes (9 sequences, 3001 rows of 1000 fp32 channels, both passes: q 1 112,
+// q 2 66, q 4 52; 33 sequences, 16384 rows of 4096: q 1 94, q 2 113, q 4 160).
+struct Pass {
+    int per_sm;       // CTAs that fit an SM
+    double round_us;  // a round of one CTA
+    int arrays;       // activations read and written
+};
+template <typename Tiles>
+Cut choose_cut(const jssm::GatedArgs &a, int es, int sms, const Pass &pass, Tiles tiles) {
+    const int64_t batch = a.batch, len = a.cu ? a.total / batch : a.seqlen;
     auto clusters = [&](int q) {
         const int64_t units = batch * tiles(q), rows = int64_t(jssm::kGatedCkpt) * q;
         int cs = 1;
-        while (cs < jssm::kGatedMaxCluster && cs * 2 <= (len + rows - 1) / rows && units * cs * 2 <= per_sm * sms)
+        while (cs < jssm::kGatedMaxCluster && cs * 2 <= (len + rows - 1) / rows &&
+               units * cs * 2 <= int64_t(pass.per_sm) * sms)
             cs *= 2;
         return Cut{q, cs, units};
     };
-    if (batch * tiles(1) >= 2 * sms) return {1, 1, batch * tiles(1)};
-    if (batch * tiles(2) * 2 >= 3 * sms) return {2, 1, batch * tiles(2)};
+    const bool ragged = a.cu && batch > 1;
+    const double all_us = double(a.total) * a.d * es * pass.arrays / 5.2e6;
+    auto alone_ok = [&](int q) {
+        return !ragged || 3.0 * len / (jssm::kGatedCkpt * q) * pass.round_us <= all_us;
+    };
+    if (batch * tiles(1) >= 2 * sms && alone_ok(1)) return {1, 1, batch * tiles(1)};
+    if (batch * tiles(2) * 2 >= 3 * sms) {
+        const int q = alone_ok(2) ? 2 : 4;
+        return {q, 1, batch * tiles(q)};
+    }
     const Cut two = clusters(2);
     return two.units * two.cs * 2 < 3 * sms ? clusters(4) : two;
 }
@@ -162,7 +181,7 @@ jamba_ssm_status launch_scan(jssm::GatedArgs &a, int32_t dtype, const DeviceInfo
     const int cp = copy_bytes(a, dtype);
     const bool bf = dtype == JAMBA_SSM_BF16, gate = a.z != nullptr;
     const int width = bf && cp >= 4 ? 64 : 32;  // channels of a warp's row
-    const Cut cut = choose_cut(a.batch, a.cu ? a.total / a.batch : a.seqlen, dev->sms, 4,
+    const Cut cut = choose_cut(a, bf ? 2 : 4, dev->sms, Pass{4, 1.4, gate ? 4 : 3},
                                [&](int q) { return int64_t(a.d + width / q - 1) / (width / q); });
     int q = cut.q, cs = cut.cs;
     void *args[] = {&a, &cs};
@@ -192,7 +211,7 @@ jamba_ssm_status launch_bwd(jssm::GatedArgs &a, int32_t dtype, const DeviceInfo 
     const int cp = copy_bytes(a, dtype);
     const bool bf = dtype == JAMBA_SSM_BF16, gate = a.z != nullptr;
     const int width = bf && cp >= 4 ? 64 : 32;
-    const Cut cut = choose_cut(a.batch, a.cu ? a.total / a.batch : a.seqlen, dev->sms, 3,
+    const Cut cut = choose_cut(a, bf ? 2 : 4, dev->sms, Pass{3, 2.8, gate ? 7 : 5},
                                [&](int q) { return int64_t(a.d + width / q - 1) / (width / q); });
     int q = cut.q, cs = cut.cs;
     void *args[] = {&a, &cs};

@@ -134,6 +134,27 @@ def test_packed_sequences_and_rows_behind_the_last(dtype, d):
     assert torch.equal(hf[0], h0[0]) and torch.equal(hf[6], h0[6])  # empty sequences
 
 
+@pytest.mark.parametrize("n", [127, 128, 129, 300])
+def test_more_packed_sequences_than_threads(n):
+    """Up to 128 sequences are taken longest first, more in their order."""
+    gen = torch.Generator().manual_seed(n)
+    lens = torch.randint(0, 40, (n,), generator=gen)
+    lens[n // 2] = 333
+    lens[0] = 0
+    total, d = int(lens.sum()), 40
+    x, g, z, rate, bias = _inputs((total, d), F32, n)
+    cu = torch.cat([torch.zeros(1, dtype=torch.long), lens.cumsum(0)]).int().to(x.device)
+    h0, dh = torch.randn(n, d, device=x.device), torch.randn(n, d, device=x.device)
+    dout = torch.randn(total, d, device=x.device)
+    ref = Reference(x, g, z, rate, bias, h0, cu=cu.tolist())
+    out, hf = jamba_ssm_gated_scan(x, g, z=z, rate=rate, bias=bias, h0=h0, cu_seqlens=cu)
+    _check_scan(ref, out, hf, f"{n} sequences")
+    got = jamba_ssm_gated_scan_bwd(x, g, dout, z=z, rate=rate, bias=bias, h0=h0, dh_final=dh,
+                                   cu_seqlens=cu)
+    for k, (v, e) in ref.gradients(dout, dh).items():
+        assert_within(got[k], v, e, k)
+
+
 def test_offsets_past_the_rows_are_clamped():
     x, g, z, rate, bias = _inputs((50, 32), F32, 2)
     cu = torch.tensor([-5, 20, 70, 1000], dtype=torch.int32, device=x.device)
