@@ -91,7 +91,7 @@ struct Cut {
 // So: one CTA to a tile where 2 (q = 1) or 1.5 (q = 2) of them come to an SM;
 // else clusters, whose barrier costs about a round's time and is hidden by the
 // other CTAs of an SM, up to the per_sm that fit one (4 of the scan's, 3 of the
-// backward's); q = 4 where that leaves under 1.5.  The backward alike: 1024
+// backward's); q = 4 where that leaves under half of them.  The backward alike: 1024
 // channels, 4096 rows, both passes: q 2 in clusters of 8 39, q 4 of 4 44, of 8 50.
 // Packed sequences are ragged: the longest, taken as three times the mean, may
 // run on alone, so q goes up until its rounds take no longer than moving all
@@ -124,7 +124,7 @@ Cut choose_cut(const jssm::GatedArgs &a, int es, int sms, const Pass &pass, Tile
         return {q, 1, batch * tiles(q)};
     }
     const Cut two = clusters(2);
-    return two.units * two.cs * 2 < 3 * sms ? clusters(4) : two;
+    return two.units * two.cs * 2 < int64_t(pass.per_sm) * sms ? clusters(4) : two;
 }
 
 using Bf = __nv_bfloat16;
