@@ -90,7 +90,7 @@ struct Cut {
 //   13 x 4096 rows x 2048:     q 1 158, q 2 165, in clusters of 8 from 247.
 // So: one CTA to a tile where 2 (q = 1) or 1.5 (q = 2) of them come to an SM;
 // else clusters, whose barrier costs about a round's time and is hidden by the
-// other CTAs of an SM, up to the per_sm that fit one (4 of the scan's, 3 of the
+// other CTAs of an SM, up to the per_sm that fit one (4 of the scan's, 2 of the
 // backward's); q = 4 where that leaves under half of them.  The backward alike: 1024
 // channels, 4096 rows, both passes: q 2 in clusters of 8 39, q 4 of 4 44, of 8 50.
 // Packed sequences are ragged: the longest, taken as three times the mean, may
@@ -211,7 +211,7 @@ jamba_ssm_status launch_bwd(jssm::GatedArgs &a, int32_t dtype, const DeviceInfo 
     const int cp = copy_bytes(a, dtype);
     const bool bf = dtype == JAMBA_SSM_BF16, gate = a.z != nullptr;
     const int width = bf && cp >= 4 ? 64 : 32;
-    const Cut cut = choose_cut(a, bf ? 2 : 4, dev->sms, Pass{3, 2.8, gate ? 7 : 5},
+    const Cut cut = choose_cut(a, bf ? 2 : 4, dev->sms, Pass{2, 2.4, gate ? 7 : 5},
                                [&](int q) { return int64_t(a.d + width / q - 1) / (width / q); });
     int q = cut.q, cs = cut.cs;
     void *args[] = {&a, &cs};
