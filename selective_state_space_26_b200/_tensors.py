@@ -20,6 +20,12 @@ def check(t, name, shape, dtype, device):
     """A contiguous tensor of this shape, dtype and device (or None)."""
     if t is None:
         return
+    try:  # the usual case first: these calls are made per token
+        if (t.dtype is dtype and t.shape == shape and t.device == device
+                and t.is_contiguous()):
+            return
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
@@ -32,13 +38,25 @@ def check(t, name, shape, dtype, device):
         raise ValueError(f"{name} must be contiguous")
 
 
-def row_stride(t, name, shape, dtype, device):
+def need(t, name, shape, dtype, device):
+    """As check, for a tensor that must be there."""
+    if t is None:
+        raise TypeError(f"{name} must be a torch.Tensor")
+    check(t, name, shape, dtype, device)
+
+
+def row_stride(t, name, shape, dtype, device, required=False):
     """Elements between the rows of an activation whose channels are contiguous
     and whose rows are evenly spaced (0 for None or a contiguous tensor)."""
-    if t is None:
+    if t is None and not required:
         return 0
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is dtype and t.shape == shape and t.device == device:  # the usual cases first
+        if t.is_contiguous():
+            return 0
+        if t.dim() == 2 and t.stride(1) == 1 and t.stride(0) >= shape[1] and shape[0] > 1:
+            return t.stride(0)
     if t.dtype != dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
     if t.shape != shape:

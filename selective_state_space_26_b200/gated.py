@@ -15,8 +15,8 @@ import torch
 
 from . import _lib
 from ._lib import JambaSSMError
-from ._tensors import (IO, check, cuda_device, empty_like, launching, ptr, raw_stream,
-                       row_stride)
+from ._tensors import (IO, check, cuda_device, empty_like, launching, need, ptr,
+                       raw_stream, row_stride)
 from ._tensors import workspace as _workspace
 
 __all__ = ["jamba_ssm_gated_scan", "jamba_ssm_gated_scan_ckpt", "jamba_ssm_gated_scan_ckpt_size",
@@ -72,7 +72,7 @@ def jamba_ssm_gated_scan(x, g, z=None, rate=None, bias=None, h0=None, out=None, 
     batch, seqlen, rows, d = _sizes(x, cu_seqlens, dev)
     io, shape = x.dtype, x.shape
     xs = row_stride(x, "x", shape, io, dev)
-    gs = row_stride(g, "g", shape, io, dev)
+    gs = row_stride(g, "g", shape, io, dev, required=True)
     zs = row_stride(z, "z", shape, io, dev)
     check(rate, "rate", (d,), _F32, dev)
     check(bias, "bias", (d,), _F32, dev)
@@ -97,8 +97,8 @@ def jamba_ssm_gated_scan(x, g, z=None, rate=None, bias=None, h0=None, out=None, 
             out = empty_like(x, xs == 0)
         if h_final is None and return_final_state and state_indices is None:
             h_final = x.new_empty(state, dtype=_F32) if h0 is None else empty_like(h0)
-        p = _lib.GatedScanParams(_SCAN, batch, seqlen, d, IO[io], 0, ptr(x), ptr(g), ptr(z), xs,
-                                 gs, zs, ptr(rate), ptr(bias), ptr(h0), ptr(out), ptr(h_final),
+        p = _lib.GatedScanParams(_SCAN, batch, seqlen, d, IO[io], 0, x.data_ptr(), g.data_ptr(),
+                                 ptr(z), xs, gs, zs, ptr(rate), ptr(bias), ptr(h0), ptr(out), ptr(h_final),
                                  ptr(cu_seqlens), rows, ptr(state_indices), ptr(initial_indices),
                                  slots, ptr(ckpt), ws, ws_bytes)
         st = _lib.gated_lib().jamba_ssm_gated_scan(byref(p), raw_stream(dev))
@@ -145,9 +145,9 @@ def jamba_ssm_gated_scan_bwd(x, g, dout, z=None, rate=None, bias=None, h0=None, 
     batch, seqlen, rows, d = _sizes(x, cu_seqlens, dev)
     io, shape = x.dtype, x.shape
     xs = row_stride(x, "x", shape, io, dev)
-    gs = row_stride(g, "g", shape, io, dev)
+    gs = row_stride(g, "g", shape, io, dev, required=True)
     zs = row_stride(z, "z", shape, io, dev)
-    check(dout, "dout", shape, io, dev)
+    need(dout, "dout", shape, io, dev)
     check(rate, "rate", (d,), _F32, dev)
     check(bias, "bias", (d,), _F32, dev)
     check(h0, "h0", (batch, d), _F32, dev)
@@ -157,16 +157,16 @@ def jamba_ssm_gated_scan_bwd(x, g, dout, z=None, rate=None, bias=None, h0=None, 
     L = _lib.gated_lib()
     with launching(stream, dev):
         if workspace is None:
-            need = L.jamba_ssm_gated_scan_bwd_workspace_size(batch, rows, d, ckpt is not None)
-            workspace = x.new_empty(need, dtype=torch.uint8)
+            size = L.jamba_ssm_gated_scan_bwd_workspace_size(batch, rows, d, ckpt is not None)
+            workspace = x.new_empty(size, dtype=torch.uint8)
         ws, ws_bytes = _workspace(workspace, dev)
         dx, dg = empty_like(dout), empty_like(dout)
         dz = None if z is None else empty_like(dout)
         drate = None if rate is None else empty_like(rate)
         dbias = None if bias is None else empty_like(bias)
         dh0 = x.new_empty((batch, d), dtype=_F32)
-        p = _lib.GatedScanBwdParams(_BWD, batch, seqlen, d, IO[io], 0, ptr(x), ptr(g), ptr(z), xs,
-                                    gs, zs, ptr(rate), ptr(bias), ptr(h0), ptr(dout),
+        p = _lib.GatedScanBwdParams(_BWD, batch, seqlen, d, IO[io], 0, x.data_ptr(), g.data_ptr(),
+                                    ptr(z), xs, gs, zs, ptr(rate), ptr(bias), ptr(h0), ptr(dout),
                                     ptr(dh_final), ptr(dx), ptr(dg), ptr(dz), ptr(drate),
                                     ptr(dbias), ptr(dh0), ptr(cu_seqlens), rows, ptr(ckpt), ws,
                                     ws_bytes)
@@ -191,23 +191,24 @@ def jamba_ssm_gated_state_update(state, x, g, z=None, rate=None, bias=None, out=
     io, shape = x.dtype, x.shape
     batch, d = shape
     xs = row_stride(x, "x", shape, io, dev)
-    gs = row_stride(g, "g", shape, io, dev)
+    gs = row_stride(g, "g", shape, io, dev, required=True)
     zs = row_stride(z, "z", shape, io, dev)
     check(rate, "rate", (d,), _F32, dev)
     check(bias, "bias", (d,), _F32, dev)
     slots = 0
     if state_indices is not None:
         check(state_indices, "state_indices", (batch,), _I32, dev)
-        slots = state.shape[0]
-    check(state, "state", (batch if state_indices is None else slots, d), _F32, dev)
+        slots = state.shape[0] if isinstance(state, torch.Tensor) else 0
+    need(state, "state", (batch if state_indices is None else slots, d), _F32, dev)
     check(out, "out", shape, io, dev)
     ws, ws_bytes = _workspace(workspace, dev)
     with launching(stream, dev):
         if out is None:
             out = empty_like(x, xs == 0)
-        p = _lib.GatedStateUpdateParams(_UPDATE, batch, d, IO[io], 0, ptr(state), ptr(x), ptr(g),
-                                        ptr(z), xs, gs, zs, ptr(rate), ptr(bias), ptr(out),
-                                        ptr(state_indices), slots, ws, ws_bytes)
+        p = _lib.GatedStateUpdateParams(_UPDATE, batch, d, IO[io], 0, state.data_ptr(),
+                                        x.data_ptr(), g.data_ptr(), ptr(z), xs, gs, zs, ptr(rate),
+                                        ptr(bias), ptr(out), ptr(state_indices), slots, ws,
+                                        ws_bytes)
         st = _lib.gated_lib().jamba_ssm_gated_state_update(byref(p), raw_stream(dev))
     if st != _lib.OK:
         _raise(st, "jamba_ssm_gated_state_update")

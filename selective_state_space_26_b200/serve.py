@@ -17,7 +17,7 @@ import torch
 
 from . import _lib
 from ._lib import JambaSSMError
-from ._tensors import IO, check, cuda_device, launching, ptr, raw_stream, row_stride
+from ._tensors import IO, check, cuda_device, launching, need, ptr, raw_stream, row_stride
 
 __all__ = ["jamba_ssm_i8_quant", "jamba_ssm_i8_proj", "jamba_ssm_batch_maps",
            "jamba_ssm_serve_get_status"]
@@ -53,7 +53,8 @@ def jamba_ssm_i8_quant(x, q=None, scale=None, stream=None):
             q = x.new_empty((*lead, pitch), dtype=_I8)
         if scale is None:
             scale = x.new_empty(lead, dtype=_F32)
-        p = _lib.I8QuantParams(_QUANT, rows, k, IO[x.dtype], 0, ptr(x), xs, ptr(q), ptr(scale))
+        p = _lib.I8QuantParams(_QUANT, rows, k, IO[x.dtype], 0, x.data_ptr(), xs, q.data_ptr(),
+                               scale.data_ptr())
         st = _lib.serve_lib().jamba_ssm_i8_quant(byref(p), raw_stream(dev))
     if st != _lib.OK:
         _raise(st, "jamba_ssm_i8_quant")
@@ -71,25 +72,25 @@ def jamba_ssm_i8_proj(q, q_scale, w, w_scale, bias=None, out=None, out_dtype=tor
     dev = cuda_device(q, "q", "jamba_ssm_i8_proj")
     if q.dim() < 1 or q.shape[-1] % 16:
         raise ValueError(f"q must be [..., a multiple of 16], got {tuple(q.shape)}")
-    if w.dim() != 2:
-        raise ValueError(f"w must be [n_out, pitch], got {tuple(w.shape)}")
+    if not isinstance(w, torch.Tensor) or w.dim() != 2:
+        raise ValueError("w must be a tensor [n_out, pitch]")
     if out is not None:
         out_dtype = out.dtype
     if out_dtype not in IO:
         raise TypeError(f"out_dtype must be bfloat16 or float32, got {out_dtype}")
     pitch, lead, n = q.shape[-1], q.shape[:-1], w.shape[0]
     check(q, "q", q.shape, _I8, dev)
-    check(q_scale, "q_scale", lead, _F32, dev)
-    check(w, "w", (n, pitch), _I8, dev)
-    check(w_scale, "w_scale", (n,), _F32, dev)
+    need(q_scale, "q_scale", lead, _F32, dev)
+    need(w, "w", (n, pitch), _I8, dev)
+    need(w_scale, "w_scale", (n,), _F32, dev)
     check(bias, "bias", (n,), _F32, dev)
     check(out, "out", (*lead, n), out_dtype, dev)
     with launching(stream, dev):
         if out is None:
             out = q.new_empty((*lead, n), dtype=out_dtype)
-        p = _lib.I8ProjParams(_PROJ, lead.numel(), pitch, n, IO[out_dtype], 0, ptr(q),
-                              ptr(q_scale), ptr(w), ptr(w_scale), ptr(bias), ptr(out),
-                              int(timeout_cycles))
+        p = _lib.I8ProjParams(_PROJ, lead.numel(), pitch, n, IO[out_dtype], 0,
+                              q.data_ptr(), q_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(),
+                              ptr(bias), out.data_ptr(), int(timeout_cycles))
         st = _lib.serve_lib().jamba_ssm_i8_proj(byref(p), raw_stream(dev))
     if st != _lib.OK:
         _raise(st, "jamba_ssm_i8_proj")
@@ -115,6 +116,10 @@ def jamba_ssm_batch_maps(new_lens, block_tables, free_blocks, request_slots, fre
     max_tokens, no free block or slot, a request longer than its table) is
     recorded in the status word (jamba_ssm_serve_get_status)."""
     dev = cuda_device(new_lens, "new_lens", "jamba_ssm_batch_maps")
+    for t, name in ((block_tables, "block_tables"), (free_blocks, "free_blocks"),
+                    (free_slots, "free_slots")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
     if new_lens.dim() != 1 or block_tables.dim() != 2:
         raise ValueError("new_lens must be [requests] and block_tables [requests, max_blocks]")
     if max_tokens is None:
@@ -124,8 +129,8 @@ def jamba_ssm_batch_maps(new_lens, block_tables, free_blocks, request_slots, fre
     n, width = new_lens.shape[0], block_tables.shape[1]
     check(new_lens, "new_lens", (n,), _I32, dev)
     check(ctx_lens, "ctx_lens", (n,), _I32, dev)
-    check(block_tables, "block_tables", (n, width), _I32, dev)
-    check(request_slots, "request_slots", (n,), _I32, dev)
+    need(block_tables, "block_tables", (n, width), _I32, dev)
+    need(request_slots, "request_slots", (n,), _I32, dev)
     check(free_blocks, "free_blocks", free_blocks.shape, _I32, dev)
     check(free_slots, "free_slots", free_slots.shape, _I32, dev)
     t = int(max_tokens)
@@ -133,14 +138,23 @@ def jamba_ssm_batch_maps(new_lens, block_tables, free_blocks, request_slots, fre
         # one buffer, the per-token maps first, each of them from a multiple of 16 bytes on
         r = -t % 4
         buf = new_lens.new_empty(4 * (t + r) + 3 * n + 5)
-        slot_map, _, pos, _, req, _, cu, si, ii, counts = buf.split(
-            (2 * t, 2 * r, t, r, t, r, n + 1, n, n, 4))
+        if r:
+            slot_map, _, pos, _, req, _, cu, si, ii, counts = buf.split_with_sizes(
+                (2 * t, 2 * r, t, r, t, r, n + 1, n, n, 4))
+        else:
+            slot_map, pos, req, cu, si, ii, counts = buf.split_with_sizes(
+                (2 * t, t, t, n + 1, n, n, 4))
         slot_map = slot_map.view(_I64)
-        p = _lib.BatchMapsParams(_MAPS, n, t, width, int(block_size), ptr(new_lens),
-                                 ptr(ctx_lens), ptr(free_blocks), free_blocks.numel(),
-                                 ptr(free_slots), free_slots.numel(), ptr(block_tables),
-                                 ptr(request_slots), ptr(cu), ptr(pos), ptr(req), ptr(slot_map),
-                                 ptr(si), ptr(ii), ptr(counts))
+        base = buf.data_ptr()
+        at_pos = base + 8 * (t + r)
+        at_req = at_pos + 4 * (t + r)
+        at_cu = at_req + 4 * (t + r)
+        at_si = at_cu + 4 * (n + 1)
+        p = _lib.BatchMapsParams(
+            _MAPS, n, t, width, int(block_size), new_lens.data_ptr(), ptr(ctx_lens),
+            free_blocks.data_ptr(), free_blocks.numel(), free_slots.data_ptr(),
+            free_slots.numel(), block_tables.data_ptr(), request_slots.data_ptr(), at_cu, at_pos,
+            at_req, base, at_si, at_si + 4 * n, at_si + 8 * n)
         st = _lib.serve_lib().jamba_ssm_batch_maps(byref(p), raw_stream(dev))
     if st != _lib.OK:
         _raise(st, "jamba_ssm_batch_maps")

@@ -451,6 +451,11 @@ def test_graph_streams_and_two_calls_at_once():
 
 def test_refusals():
     x, g, z, rate, bias = _inputs((2, 10, 16), F32, 1)
+    for call in (lambda: jamba_ssm_gated_scan(x, None),
+                 lambda: jamba_ssm_gated_scan_bwd(x, g, None),
+                 lambda: jamba_ssm_gated_state_update(None, x[0], g[0])):
+        with pytest.raises(TypeError, match="torch.Tensor"):
+            call()
     with pytest.raises(ValueError, match="CUDA"):
         jamba_ssm_gated_scan(x.cpu(), g.cpu())
     with pytest.raises(TypeError):
