@@ -20,6 +20,7 @@ struct I8ProjArgs {
     void *out;
     int ntok, n, kblocks;  // kblocks: 128-byte blocks of K
     int ks;                // CTAs that share a tile's K (the split kernel)
+    bool pairs;            // two bf16 channels can be written as a word
     uint64_t limit;
 };
 
@@ -28,6 +29,56 @@ struct I8ProjArgs {
 __device__ __forceinline__ float i8_scaled(int acc, float s, float w) {
     const bool less = s < w;
     return static_cast<float>(acc) * (less ? s : w) * (less ? w : s);
+}
+// Scales between 2^-60 and 2^60, and 0: any order of the factors will do.
+__device__ __forceinline__ bool i8_tame(float s) {
+    return s == 0.0f || (s >= 0x1p-60f && s <= 0x1p60f);
+}
+
+// Columns [0, cols) of a lane's channel (tokens `out` on, n elements apart) from
+// COLS accumulators.  `tame`: every scale is.  `pairs` (bf16, n even and the
+// rows 4-byte aligned): neighbouring lanes exchange every other column, so that
+// each writes two channels of one token as a word, and a warp's store 16 words
+// of two tokens: half the store instructions, which with the rest of this loop
+// bound the kernel's tiles where K is short.
+template <typename T, bool TAME, bool WHOLE, int COLS>
+__device__ __forceinline__ void i8_columns(T *out, int64_t n, const uint32_t (&v)[COLS], const float *sc,
+                                           float w, float bias, bool on, int cols, bool pairs) {
+    auto value = [&](int i) {
+        const float s = sc[i];
+        const float p = TAME ? static_cast<float>(int(v[i])) * s * w : i8_scaled(int(v[i]), s, w);
+        return p + bias;
+    };
+    if constexpr (sizeof(T) == 2) {
+        if (pairs) {
+            const bool odd = threadIdx.x & 1;
+            T *at = odd ? out + n - 1 : out;
+#pragma unroll
+            for (int i = 0; i < COLS; i += 2) {
+                const float a = value(i), b = value(i + 1);
+                const float got = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
+                const uint32_t word = pack_bf16x2(odd ? got : a, odd ? b : got);
+                if (WHOLE || (on && i + int(odd) < cols)) *reinterpret_cast<uint32_t *>(at) = word;
+                at += 2 * n;
+            }
+            return;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < COLS; ++i) {
+        if (WHOLE || (on && i < cols)) *out = from_f32<T>(value(i));
+        out += n;
+    }
+}
+template <typename T, int COLS>
+__device__ __forceinline__ void i8_put(T *out, int64_t n, const uint32_t (&v)[COLS], const float *sc, float w,
+                                       float bias, bool on, int cols, bool tame, bool pairs) {
+    tame = __all_sync(0xffffffffu, tame && i8_tame(w));
+    const bool whole = __all_sync(0xffffffffu, on && cols >= COLS);
+    if (tame && whole)
+        i8_columns<T, true, true>(out, n, v, sc, w, bias, on, cols, pairs);
+    else
+        i8_columns<T, false, false>(out, n, v, sc, w, bias, on, cols, pairs);
 }
 
 constexpr uint32_t i8_idesc(int m, int n) {
@@ -115,12 +166,6 @@ struct I8Wait {
     }
 };
 
-// One output of a lane's channel.
-template <typename T>
-__device__ __forceinline__ void i8_put(T *out, int acc, float s, float w, float bias) {
-    *out = from_f32<T>(i8_scaled(acc, s, w) + bias);
-}
-
 // ------------------------------------------------------------- many tokens
 // Persistent CTA pairs on tiles of 256 channels x 256 tokens: one MMA spans the
 // pair (cta_group::2), each CTA staging its 128 channels and 128 of the tokens,
@@ -137,7 +182,8 @@ struct I8PairCfg {
     static constexpr int kOffScale = kStages * kStage;            // 2 x 256 token scales
     static constexpr int kOffBar = kOffScale + 2 * kTile * 4;
     static constexpr int kSmem = kOffBar + 256 + 1024;            // and up to 1024 to align
-    static constexpr int kThreads = 192;            // copies, MMAs, 4 warps of outputs
+    static constexpr int kOutWarps = 8;             // two to a quarter of the TMEM lanes
+    static constexpr int kThreads = 64 + 32 * kOutWarps;  // and the copies' warp and the MMAs'
     static constexpr uint32_t kIdesc = i8_idesc(256, 256);
 };
 
@@ -169,7 +215,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(I8PairCfg::kThreads,
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&acc_full[b], 1);
-            mbar_init(&acc_empty[b], 8);  // 4 warps of both CTAs
+            mbar_init(&acc_empty[b], 2 * C::kOutWarps);  // both CTAs'
         }
         mbar_init(drain, 1);
         *abort_flag = 0;
@@ -244,7 +290,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(I8PairCfg::kThreads,
         }
         __syncwarp();
     } else {
-        const int q = warp & 3;  // this warp's TMEM lanes: 32 q ..
+        // this warp's TMEM lanes, 32 q .. 32 q + 31, and its half of the columns
+        constexpr int kOut = 32 * C::kOutWarps, kCols = C::kTile / (C::kOutWarps / 4);
+        const int q = warp & 3, c0 = (warp - 2) / 4 * kCols;
         int j = 0;
         for (int64_t it = pair; it < tiles; it += pairs, ++j) {
             const int buf = j & 1;
@@ -253,23 +301,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(I8PairCfg::kThreads,
             const bool on = o < a.n;
             const float w = on ? a.ws[o] : 0.0f, bias = on && a.bias ? a.bias[o] : 0.0f;
             float *sc = scales + buf * C::kTile;
-            for (int i = threadIdx.x - 64; i < C::kTile; i += 128)
+            bool tame = true;
+            for (int i = threadIdx.x - 64; i < C::kTile; i += kOut) {
                 sc[i] = m0 + i < a.ntok ? a.qs[m0 + i] : 0.0f;
-            const bool got = wait(&acc_full[buf], (j / 2) & 1);
-            if (!epilogue_all(got, 128)) break;  // and the scales are staged
+                tame = tame && i8_tame(sc[i]);
+            }
+            tame = epilogue_all(tame, kOut);  // and the scales are staged
+            if (!epilogue_all(wait(&acc_full[buf], (j / 2) & 1), kOut)) break;
             tc_fence_after();
             T *out = static_cast<T *>(a.out) + int64_t(m0) * a.n + o;
             const int cols = min(C::kTile, a.ntok - m0);
+            const uint32_t at = tmem + (uint32_t(q * 32) << 16) + uint32_t(buf * C::kTile);
 #pragma unroll 1
-            for (int c = 0; c < cols; c += 32) {
-                float v[32];
-                tmem_ld32(tmem + (uint32_t(q * 32) << 16) + uint32_t(buf * C::kTile + c), v);
+            for (int c = c0; c < min(c0 + kCols, cols); c += 32) {
+                float f[32];
+                tmem_ld32(at + uint32_t(c), f);
+                uint32_t v[32];
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    if (on && c + i < cols)
-                        i8_put<T>(out, __float_as_int(v[i]), sc[c + i], w, bias);
-                    out += a.n;
-                }
+                for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(f[i]);
+                i8_put<T>(out + int64_t(c) * a.n, a.n, v, sc + c, w, bias, on, cols - c, tame, a.pairs);
             }
             tc_fence_before();
             __syncwarp();
@@ -399,10 +449,7 @@ __global__ void __launch_bounds__(I8SplitCfg<NT>::kThreads, 1)
                 tmem_ld16_async(lanes + c, v);
                 tmem_wait_ld();
                 tmem_regs_ready(v);
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (on && c + i < cols)
-                        i8_put<T>(out + int64_t(c + i) * a.n, int(v[i]), scales[c + i], w, bias);
+                i8_put<T>(out + int64_t(c) * a.n, a.n, v, scales + c, w, bias, on, cols - c, false, a.pairs);
             }
         }
     } else {
@@ -439,7 +486,7 @@ __global__ void __launch_bounds__(I8SplitCfg<NT>::kThreads, 1)
             }
         }
         cluster_barrier();
-        if (warp >= 2 && on) {
+        if (warp >= 2) {
             const int c0 = rank * own, end = min(c0 + own, cols);
             if (own >= 4) {
                 const int4 *mine = reinterpret_cast<const int4 *>(sums) + q * 32 + lane;
@@ -450,11 +497,9 @@ __global__ void __launch_bounds__(I8SplitCfg<NT>::kThreads, 1)
                         t.x += p.x, t.y += p.y, t.z += p.z, t.w += p.w;
                     }
                     mine += a.ks * C::kM;
-                    const int acc[4] = {t.x, t.y, t.z, t.w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (c + i < end)
-                            i8_put<T>(out + int64_t(c + i) * a.n, acc[i], scales[c + i], w, bias);
+                    const uint32_t acc[4] = {uint32_t(t.x), uint32_t(t.y), uint32_t(t.z), uint32_t(t.w)};
+                    i8_put<T>(out + int64_t(c) * a.n, a.n, acc, scales + c, w, bias, on, end - c, false,
+                              a.pairs);
                 }
             } else {
                 const int2 *mine = reinterpret_cast<const int2 *>(sums) + q * 32 + lane;
@@ -463,8 +508,8 @@ __global__ void __launch_bounds__(I8SplitCfg<NT>::kThreads, 1)
                     const int2 p = mine[r * C::kM];
                     t.x += p.x, t.y += p.y;
                 }
-                if (c0 < end) i8_put<T>(out + int64_t(c0) * a.n, t.x, scales[c0], w, bias);
-                if (c0 + 1 < end) i8_put<T>(out + int64_t(c0 + 1) * a.n, t.y, scales[c0 + 1], w, bias);
+                const uint32_t acc[2] = {uint32_t(t.x), uint32_t(t.y)};
+                i8_put<T>(out + int64_t(c0) * a.n, a.n, acc, scales + c0, w, bias, on, end - c0, false, a.pairs);
             }
         }
     }

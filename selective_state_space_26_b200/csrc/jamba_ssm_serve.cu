@@ -56,7 +56,7 @@ bool encode_bytes(EncodeTiledFn fn, CUtensorMap *map, const void *ptr, int64_t p
 
 struct Kernel {
     const void *fn;
-    int smem;
+    int smem, threads;
 };
 
 // Raises a kernel's dynamic shared-memory limit, once per kernel and device.
@@ -88,10 +88,10 @@ template <typename T> const void *quant_kernel(int lanes, bool vec) {
 
 template <typename T> Kernel split_kernel(int nt) {
     switch (nt) {
-        case 16: return {(const void *)&jssm::i8_proj_split_kernel<T, 16>, jssm::I8SplitCfg<16>::kSmem};
-        case 32: return {(const void *)&jssm::i8_proj_split_kernel<T, 32>, jssm::I8SplitCfg<32>::kSmem};
-        case 64: return {(const void *)&jssm::i8_proj_split_kernel<T, 64>, jssm::I8SplitCfg<64>::kSmem};
-        default: return {(const void *)&jssm::i8_proj_split_kernel<T, 128>, jssm::I8SplitCfg<128>::kSmem};
+        case 16: return {(const void *)&jssm::i8_proj_split_kernel<T, 16>, jssm::I8SplitCfg<16>::kSmem, 192};
+        case 32: return {(const void *)&jssm::i8_proj_split_kernel<T, 32>, jssm::I8SplitCfg<32>::kSmem, 192};
+        case 64: return {(const void *)&jssm::i8_proj_split_kernel<T, 64>, jssm::I8SplitCfg<64>::kSmem, 192};
+        default: return {(const void *)&jssm::i8_proj_split_kernel<T, 128>, jssm::I8SplitCfg<128>::kSmem, 192};
     }
 }
 
@@ -175,6 +175,7 @@ JSSM_SERVE_API jamba_ssm_status jamba_ssm_i8_proj(const jamba_ssm_i8_proj_params
     a.kblocks = static_cast<int>(ceil_div(pitch, 128));
     a.limit = p.timeout_cycles ? p.timeout_cycles : kDefaultTimeoutCycles;
     const bool bf = p.out_dtype == JAMBA_SSM_BF16;
+    a.pairs = bf && p.n_out % 2 == 0 && aligned(p.out, 4);
     CUtensorMap map_w, map_q;
     if (!encode_bytes(fn, &map_w, p.w, pitch, p.n_out, 128)) return cuda_fail(cudaErrorInvalidValue);
 
@@ -184,8 +185,10 @@ JSSM_SERVE_API jamba_ssm_status jamba_ssm_i8_proj(const jamba_ssm_i8_proj_params
     int64_t grid;
     if (pair) {
         if (!encode_bytes(fn, &map_q, p.q, pitch, p.ntok, 128)) return cuda_fail(cudaErrorInvalidValue);
-        k = bf ? Kernel{(const void *)&jssm::i8_proj_pair_kernel<__nv_bfloat16>, jssm::I8PairCfg::kSmem}
-               : Kernel{(const void *)&jssm::i8_proj_pair_kernel<float>, jssm::I8PairCfg::kSmem};
+        k = bf ? Kernel{(const void *)&jssm::i8_proj_pair_kernel<__nv_bfloat16>, jssm::I8PairCfg::kSmem,
+                    jssm::I8PairCfg::kThreads}
+               : Kernel{(const void *)&jssm::i8_proj_pair_kernel<float>, jssm::I8PairCfg::kSmem,
+                    jssm::I8PairCfg::kThreads};
         const int64_t pairs = dev->sms / 2;
         grid = 2 * (pair_tiles < pairs ? pair_tiles : pairs);
         a.ks = 1;  // the kernel has its own cluster of 2
@@ -202,7 +205,7 @@ JSSM_SERVE_API jamba_ssm_status jamba_ssm_i8_proj(const jamba_ssm_i8_proj_params
     const cudaError_t e = raise_smem(k, dev->id);
     if (e != cudaSuccess) return cuda_fail(e);
     void *args[] = {&map_w, &map_q, &a};
-    st = launch_early(k.fn, dim3(unsigned(grid)), 192, k.smem, a.ks, args, stream);
+    st = launch_early(k.fn, dim3(unsigned(grid)), unsigned(k.threads), k.smem, a.ks, args, stream);
     return st != JAMBA_SSM_OK ? st : finish_launch(stream, nullptr);
 }
 
