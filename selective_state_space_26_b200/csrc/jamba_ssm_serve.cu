@@ -97,6 +97,42 @@ template <typename T> Kernel split_kernel(int nt) {
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// Tokens of a tile and CTAs to a tile's K; nt = 0: the pairs' kernel.
+struct ProjCut {
+    int nt, ks;
+    int64_t tiles;
+};
+
+// The cut that should take the least time.  Measured, in us: a 128-byte block of
+// K takes a CTA 0.3 whatever the tokens (its 128 rows of the weight come from
+// HBM as single lines); a tile's start, first copy and outputs 2 + nt / 64; the
+// exchange of a split K 1.3; the pairs' kernel 5 once and a round of its tiles
+// 0.26 a block, or 3.5 where the outputs take longer.  A wave is as many CTAs as
+// run at once, with clusters of 4 and 8 fewer than the SMs, whose groups they
+// leave partly empty (128 x 1024 x 1024 in 8 ways: 9.6 us for 128 tokens, one
+// wave, 17 for 200, two).  E.g. 200 tokens, K 1024, 1024 channels: 64-token
+// tiles in 4 ways 7.5, 128-token tiles in 4 and 8 ways 9.1 and 14, pairs 10.
+ProjCut choose_proj(int64_t ntok, int64_t n_out, int kblocks, int sms) {
+    ProjCut best{0, 1, ceil_div(n_out, 256) * ceil_div(ntok, 256)};
+    const double round = 0.26 * kblocks > 3.5 ? 0.26 * kblocks : 3.5;
+    double least = ntok <= 64 ? 1e30 : 5.0 + double(ceil_div(best.tiles, sms / 2)) * round;
+    for (int nt : {16, 32, 64, 128}) {
+        if (nt < 64 && ntok > nt) continue;  // 16 and 32 for that few tokens only
+        const int64_t tiles = ceil_div(n_out, 128) * ceil_div(ntok, nt);
+        for (int ks = 1; ks <= jssm::kI8MaxSplit && ks <= kblocks; ks *= 2) {
+            const int64_t at_once = ks == 8 ? sms * 3 / 4 : ks == 4 ? sms * 15 / 16 : sms;
+            const double us = double(ceil_div(tiles * ks, at_once)) *
+                              (2.0 + nt / 64.0 + 0.3 * double(ceil_div(kblocks, ks)) + (ks > 1 ? 1.3 : 0.0));
+            if (us < least) {
+                least = us;
+                best = {nt, ks, tiles};
+            }
+        }
+        if (ntok <= nt) break;  // more columns would be empty
+    }
+    return best;
+}
+
 bool io_dtype(int32_t d) { return d == JAMBA_SSM_BF16 || d == JAMBA_SSM_F32; }
 
 }  // namespace
@@ -179,29 +215,23 @@ JSSM_SERVE_API jamba_ssm_status jamba_ssm_i8_proj(const jamba_ssm_i8_proj_params
     CUtensorMap map_w, map_q;
     if (!encode_bytes(fn, &map_w, p.w, pitch, p.n_out, 128)) return cuda_fail(cudaErrorInvalidValue);
 
-    const int64_t pair_tiles = ceil_div(p.n_out, 256) * ceil_div(p.ntok, 256);
-    const bool pair = p.ntok > 128 && pair_tiles * 4 >= dev->sms;
     Kernel k;
     int64_t grid;
-    if (pair) {
+    const ProjCut cut = choose_proj(p.ntok, p.n_out, a.kblocks, dev->sms);
+    if (cut.nt == 0) {
         if (!encode_bytes(fn, &map_q, p.q, pitch, p.ntok, 128)) return cuda_fail(cudaErrorInvalidValue);
         k = bf ? Kernel{(const void *)&jssm::i8_proj_pair_kernel<__nv_bfloat16>, jssm::I8PairCfg::kSmem,
-                    jssm::I8PairCfg::kThreads}
+                        jssm::I8PairCfg::kThreads}
                : Kernel{(const void *)&jssm::i8_proj_pair_kernel<float>, jssm::I8PairCfg::kSmem,
-                    jssm::I8PairCfg::kThreads};
-        const int64_t pairs = dev->sms / 2;
-        grid = 2 * (pair_tiles < pairs ? pair_tiles : pairs);
-        a.ks = 1;  // the kernel has its own cluster of 2
+                        jssm::I8PairCfg::kThreads};
+        grid = 2 * (cut.tiles < dev->sms / 2 ? cut.tiles : dev->sms / 2);
     } else {
-        const int nt = p.ntok <= 16 ? 16 : p.ntok <= 32 ? 32 : p.ntok <= 64 ? 64 : 128;
-        if (!encode_bytes(fn, &map_q, p.q, pitch, p.ntok, nt)) return cuda_fail(cudaErrorInvalidValue);
-        k = bf ? split_kernel<__nv_bfloat16>(nt) : split_kernel<float>(nt);
-        const int64_t tiles = ceil_div(p.n_out, 128) * ceil_div(p.ntok, nt);
-        a.ks = 1;
-        while (a.ks < jssm::kI8MaxSplit && a.ks * 2 <= a.kblocks && tiles * a.ks * 2 <= dev->sms) a.ks *= 2;
-        grid = tiles * a.ks;
+        if (!encode_bytes(fn, &map_q, p.q, pitch, p.ntok, cut.nt)) return cuda_fail(cudaErrorInvalidValue);
+        k = bf ? split_kernel<__nv_bfloat16>(cut.nt) : split_kernel<float>(cut.nt);
+        grid = cut.tiles * cut.ks;
         if (grid > 0x7fffffff) return JAMBA_SSM_ERR_UNSUPPORTED;
     }
+    a.ks = cut.ks;  // 1 for the pairs' kernel, which has its own cluster of 2
     const cudaError_t e = raise_smem(k, dev->id);
     if (e != cudaSuccess) return cuda_fail(e);
     void *args[] = {&map_w, &map_q, &a};
