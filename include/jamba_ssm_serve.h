@@ -67,7 +67,10 @@ jamba_ssm_status jamba_ssm_i8_quant(const jamba_ssm_i8_quant_params *p, void *st
  *   out      [ntok, n_out] out_dtype, contiguous; overlaps no input.
  * ntok in [0, 2^31 - 2^16], n_out in [1, 2^24], k in [1, JAMBA_SSM_I8_MAX_K].
  * timeout_cycles: limit of the kernel's waits in SM clock cycles (0 = about
- * 2 s); a wait that ran out is recorded as JAMBA_SSM_ERR_TIMEOUT.
+ * 2 s); a wait that ran out is recorded as JAMBA_SSM_ERR_TIMEOUT, and the
+ * outputs are not all written then.  debug_flags: 0 in production; bit 0
+ * withholds every CTA's first copies, so that its waits run out (the test of
+ * that path).
  */
 typedef struct jamba_ssm_i8_proj_params {
     size_t struct_size;              /* = sizeof(jamba_ssm_i8_proj_params) */
@@ -81,6 +84,7 @@ typedef struct jamba_ssm_i8_proj_params {
     const float *bias;
     void *out;
     uint64_t timeout_cycles;
+    uint32_t debug_flags;
 } jamba_ssm_i8_proj_params;
 
 jamba_ssm_status jamba_ssm_i8_proj(const jamba_ssm_i8_proj_params *p, void *stream);

@@ -216,7 +216,8 @@ class I8ProjParams(ctypes.Structure):
     _fields_ = _fields(
         struct_size=ctypes.c_size_t, ntok=ctypes.c_int64, k=ctypes.c_int64, n_out=ctypes.c_int64,
         out_dtype=ctypes.c_int32, reserved=ctypes.c_int32, q=_vp, q_scale=_fp, w=_vp,
-        w_scale=_fp, bias=_fp, out=_vp, timeout_cycles=ctypes.c_uint64)
+        w_scale=_fp, bias=_fp, out=_vp, timeout_cycles=ctypes.c_uint64,
+        debug_flags=ctypes.c_uint32)
 
 
 class BatchMapsParams(ctypes.Structure):

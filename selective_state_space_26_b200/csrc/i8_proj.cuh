@@ -21,6 +21,7 @@ struct I8ProjArgs {
     int ntok, n, kblocks;  // kblocks: 128-byte blocks of K
     int ks;                // CTAs that share a tile's K (the split kernel)
     bool pairs;            // two bf16 channels can be written as a word
+    bool withhold;         // test of the bounded waits: leave out the first copies
     uint64_t limit;
 };
 
@@ -245,6 +246,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(I8PairCfg::kThreads,
                         ok = false;
                         break;
                     }
+                    if (a.withhold && wi == 0) continue;
                     uint8_t *st = smem + s * C::kStage;
                     if (leader) mbar_arrive_expect_tx(&full[s], 2 * C::kStage);
                     const uint32_t bar = mapa(smem_u32(&full[s]), 0);
@@ -405,6 +407,7 @@ __global__ void __launch_bounds__(I8SplitCfg<NT>::kThreads, 1)
             for (; issued < cnt; ++issued) {
                 const int s = issued % C::kStages;
                 if (issued >= C::kStages && !wait(&empty[s], ((issued / C::kStages) & 1) ^ 1)) break;
+                if (a.withhold && issued == 0) continue;
                 uint8_t *st = smem + s * C::kStage;
                 mbar_arrive_expect_tx(&full[s], C::kStage);
                 tma_load_2d(st, &map_w, (kb0 + issued) * 128, n0, &full[s]);

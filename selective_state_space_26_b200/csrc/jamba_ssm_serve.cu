@@ -210,6 +210,7 @@ JSSM_SERVE_API jamba_ssm_status jamba_ssm_i8_proj(const jamba_ssm_i8_proj_params
     a.n = static_cast<int>(p.n_out);
     a.kblocks = static_cast<int>(ceil_div(pitch, 128));
     a.limit = p.timeout_cycles ? p.timeout_cycles : kDefaultTimeoutCycles;
+    a.withhold = (p.debug_flags & 1u) != 0;
     const bool bf = p.out_dtype == JAMBA_SSM_BF16;
     a.pairs = bf && p.n_out % 2 == 0 && aligned(p.out, 4);
     CUtensorMap map_w, map_q;

@@ -62,7 +62,7 @@ def jamba_ssm_i8_quant(x, q=None, scale=None, stream=None):
 
 
 def jamba_ssm_i8_proj(q, q_scale, w, w_scale, bias=None, out=None, out_dtype=torch.bfloat16,
-                      timeout_cycles: int = 0, stream=None):
+                      timeout_cycles: int = 0, stream=None, debug_flags: int = 0):
     """out = (q . w) * q_scale * w_scale + bias, the sum exact in 32-bit
     integers, rounded once to out_dtype (bf16 or fp32).
 
@@ -90,7 +90,7 @@ def jamba_ssm_i8_proj(q, q_scale, w, w_scale, bias=None, out=None, out_dtype=tor
             out = q.new_empty((*lead, n), dtype=out_dtype)
         p = _lib.I8ProjParams(_PROJ, lead.numel(), pitch, n, IO[out_dtype], 0,
                               q.data_ptr(), q_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(),
-                              ptr(bias), out.data_ptr(), int(timeout_cycles))
+                              ptr(bias), out.data_ptr(), int(timeout_cycles), int(debug_flags))
         st = _lib.serve_lib().jamba_ssm_i8_proj(byref(p), raw_stream(dev))
     if st != _lib.OK:
         _raise(st, "jamba_ssm_i8_proj")

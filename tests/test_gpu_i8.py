@@ -195,6 +195,21 @@ def test_graph_and_streams():
     assert torch.equal(out, want_old)
 
 
+@pytest.mark.parametrize("m,k,n", [(8, 1024, 256), (8, 4096, 300), (100, 256, 128), (900, 2048, 4096)])
+def test_waits_that_run_out_are_reported(m, k, n):
+    """The first copies withheld: the kernel gives its waits up, records the
+    timeout and ends; the next call is whole again."""
+    g = _gen(3)
+    q, s = jamba_ssm_i8_quant(torch.randn(m, k, generator=g, device="cuda"))
+    w, ws = jamba_ssm_i8_quant(torch.randn(n, k, generator=g, device="cuda"))
+    good = jamba_ssm_i8_proj(q, s, w, ws)
+    assert jamba_ssm_serve_get_status() == 0
+    jamba_ssm_i8_proj(q, s, w, ws, timeout_cycles=2_000_000, debug_flags=1)
+    assert jamba_ssm_serve_get_status() == _lib.ERR_TIMEOUT
+    assert torch.equal(jamba_ssm_i8_proj(q, s, w, ws), good)
+    assert jamba_ssm_serve_get_status() == 0
+
+
 def test_refusals():
     g = _gen(1)
     q, s = jamba_ssm_i8_quant(torch.randn(4, 32, generator=g, device="cuda"))
