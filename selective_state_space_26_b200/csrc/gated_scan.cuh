@@ -353,6 +353,7 @@ __global__ void __launch_bounds__(kGatedThreads, 4) gated_scan_kernel(const Gate
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int col = lane % LPR, run = lane / LPR;
     if (!CLUSTER) cs = 1;
+    if (CLUSTER) cluster_arrive();  // waited for before the first store to another CTA
     const int rank = CLUSTER ? static_cast<int>(cluster_rank()) : 0;
     const int tiles = (a.d + LPR * VEC - 1) / (LPR * VEC);
     const int64_t unit = blockIdx.x / cs;
@@ -418,6 +419,7 @@ __global__ void __launch_bounds__(kGatedThreads, 4) gated_scan_kernel(const Gate
     float *ck = warp % (W / Q) == 0 && run == 0 && on && a.ckpt
                     ? a.ckpt + (row0 / kGatedCkpt + b + t / kGatedCkpt) * a.d + c
                     : nullptr;
+    if (CLUSTER) cluster_wait();  // every CTA of the cluster has started
     for (int k = 0; k < rounds; ++k, t += stride) {
         const int par = k & 1;
         const bool full = len - t >= S * Q;

@@ -48,6 +48,7 @@ template <bool GATE> struct GatedBwdCfg {
     static constexpr int kSmemBytes = kGatedBwdWarps * 2 * kStageBytes;
 };
 
+#pragma nv_diag_suppress 549  // s[i] and dy[i] are set just before `ahead` reads them
 template <typename T, int VEC, bool GATE, int Q, int CP, bool CLUSTER>
 __global__ void __launch_bounds__(kGatedBwdThreads, 2) gated_scan_bwd_kernel(const GatedArgs a, int cs) {
     using Raw = GatedRaw<T, VEC>;
@@ -66,6 +67,7 @@ __global__ void __launch_bounds__(kGatedBwdThreads, 2) gated_scan_bwd_kernel(con
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int col = lane % LPR, run = lane / LPR;
     if (!CLUSTER) cs = 1;
+    if (CLUSTER) cluster_arrive();  // waited for before the first store to another CTA
     const int rank = CLUSTER ? static_cast<int>(cluster_rank()) : 0;
     const int tiles = (a.d + LPR * VEC - 1) / (LPR * VEC);
     const int64_t unit = blockIdx.x / cs;
@@ -123,6 +125,7 @@ __global__ void __launch_bounds__(kGatedBwdThreads, 2) gated_scan_bwd_kernel(con
     };
     L block = checkpoint(t);
     int64_t o0 = (row0 + t + run * S) * a.d + c;  // the lane's first output
+    if (CLUSTER) cluster_wait();  // every CTA of the cluster has started
     for (int k = 0; k < rounds; ++k, t -= stride) {
         const int par = k & 1;
         const bool full = len - t >= S * Q;
