@@ -303,7 +303,7 @@ __device__ __forceinline__ Lane2 lshfl_down(Lane2 a, int by) {
 // as (P2, b2) after (P1, b1) = (P2 P1, b2 + P2 b1).
 //
 // A lane takes a run of S = 16 rows of its channels; a warp holds Q runs side by
-// side, a CTA's 4 warps a chunk of 64 Q rows, the CTAs of a cluster consecutive
+// side, a CTA's W = 4 or 8 warps a chunk of 16 W Q rows, the CTAs of a cluster consecutive
 // chunks, and the cluster walks its sequence in strides of all of them.  Each
 // lane forms its rows' states from zero and products in registers; a shuffle,
 // one exchange through shared memory and one through the cluster's distributed
@@ -321,30 +321,32 @@ __device__ __forceinline__ Lane2 lshfl_down(Lane2 a, int by) {
 // What bounds it: HBM in fp32 (4096 x 4096 with z: 44 us, 6.1 TB/s); in bf16,
 // where an element is half the bytes for the same arithmetic, the issue slots
 // and the special-function pipe come close (13 x 4096 x 2048: 158 us, 5.5 TB/s;
-// 8192 channels by 4096 rows, with 256 tiles on 148 SMs: 60 us, 4.5 TB/s).  The
+// 8192 channels by 4096 rows, with 256 tiles on 148 SMs: 57 us, 4.7 TB/s).  The
 // steps there, us at 13 x 4096 x 2048: runs of 8 rows and 8 warps 174, without
 // the copies 143, without the sigmoids too 107; runs of 16 and 4 warps, which
 // halve the exchange's share of a row, 158.  A reciprocal for each sigmoid, and
 // three or four stages instead of two, were slower or no faster.
 constexpr int kGatedMaxCluster = 8;
-constexpr int kGatedWarps = 4, kGatedRun = 16, kGatedThreads = 32 * kGatedWarps;
-static_assert(kGatedWarps * kGatedRun == kGatedCkpt, "a checkpoint before every W / Q warps' rows");
+constexpr int kGatedRun = 16;
 
-template <bool GATE> struct GatedScanCfg {
+template <bool GATE, int W> struct GatedScanCfg {
+    static constexpr int kThreads = 32 * W;
     static constexpr int kArrays = GATE ? 3 : 2;
     static constexpr int kArrayBytes = kGatedRun * 128;  // one array's rows of one warp
     static constexpr int kStageBytes = kArrays * kArrayBytes;
-    static constexpr int kSmemBytes = kGatedWarps * 2 * kStageBytes;
+    static constexpr int kSmemBytes = W * 2 * kStageBytes;
 };
 
-template <typename T, int VEC, bool GATE, int Q, int CP, bool CLUSTER>
-__global__ void __launch_bounds__(kGatedThreads, 4) gated_scan_kernel(const GatedArgs a, int cs) {
+template <typename T, int VEC, bool GATE, int Q, int CP, bool CLUSTER, int W>
+__global__ void __launch_bounds__(32 * W, 16 / W) gated_scan_kernel(const GatedArgs a, int cs) {
     using Raw = GatedRaw<T, VEC>;
     using R = typename Raw::type;
-    using C = GatedScanCfg<GATE>;
+    using C = GatedScanCfg<GATE, W>;
     using L = Lane<VEC>;
     using Map = RunMap<VEC>;
-    constexpr int S = kGatedRun, W = kGatedWarps, LPR = 32 / Q, kChunk = W * S * Q;
+    constexpr int S = kGatedRun, LPR = 32 / Q, kChunk = W * S * Q;
+    constexpr int kBlockWarps = kGatedCkpt / (S * Q);  // warps of a checkpoint's 64 rows
+    static_assert(kBlockWarps >= 1 && W % kBlockWarps == 0, "");
     using F = GatedFeed<T, VEC, S, Q, CP>;
     extern __shared__ __align__(128) uint8_t stages[];
     __shared__ Map runs[2][W][LPR];
@@ -357,8 +359,8 @@ __global__ void __launch_bounds__(kGatedThreads, 4) gated_scan_kernel(const Gate
     const int rank = CLUSTER ? static_cast<int>(cluster_rank()) : 0;
     const int tiles = (a.d + LPR * VEC - 1) / (LPR * VEC);
     const int64_t unit = blockIdx.x / cs;
-    __shared__ int order[kGatedThreads + 1];
-    const int b = gated_sequence<kGatedThreads>(a, static_cast<int>(unit / tiles), order);
+    __shared__ int order[C::kThreads + 1];
+    const int b = gated_sequence<C::kThreads>(a, static_cast<int>(unit / tiles), order);
     const int c0 = static_cast<int>(unit % tiles) * LPR * VEC, c = c0 + col * VEC;
     const bool on = c < a.d;
 
@@ -415,8 +417,7 @@ __global__ void __launch_bounds__(kGatedThreads, 4) gated_scan_kernel(const Gate
     const L one = L::of(1.0f), zero = L::of(0.0f);
     T *op = static_cast<T *>(a.out) + (row0 + t + run * S) * a.d + c;
     const bool store = on && a.out;
-    // a checkpoint is the state before 64 rows, which W / Q warps take
-    float *ck = warp % (W / Q) == 0 && run == 0 && on && a.ckpt
+    float *ck = warp % kBlockWarps == 0 && run == 0 && on && a.ckpt
                     ? a.ckpt + (row0 / kGatedCkpt + b + t / kGatedCkpt) * a.d + c
                     : nullptr;
     if (CLUSTER) cluster_wait();  // every CTA of the cluster has started

@@ -162,19 +162,27 @@ jamba_ssm_status launch_clusters(const Kernel &k, int64_t units, int cs, void **
                   args, stream);
 }
 
-template <typename T, int VEC, int CP, int Q, bool CL> Kernel scan_kernel_q(bool gate) {
-    return gate ? Kernel{(const void *)&jssm::gated_scan_kernel<T, VEC, true, Q, CP, CL>,
-                         jssm::kGatedThreads, jssm::GatedScanCfg<true>::kSmemBytes}
-                : Kernel{(const void *)&jssm::gated_scan_kernel<T, VEC, false, Q, CP, CL>,
-                         jssm::kGatedThreads, jssm::GatedScanCfg<false>::kSmemBytes};
+template <typename T, int VEC, int CP, int Q, bool CL, int W> Kernel scan_kernel_w(bool gate) {
+    using G = jssm::GatedScanCfg<true, W>;
+    using N = jssm::GatedScanCfg<false, W>;
+    return gate ? Kernel{(const void *)&jssm::gated_scan_kernel<T, VEC, true, Q, CP, CL, W>, G::kThreads,
+                         G::kSmemBytes}
+                : Kernel{(const void *)&jssm::gated_scan_kernel<T, VEC, false, Q, CP, CL, W>, N::kThreads,
+                         N::kSmemBytes};
 }
-template <typename T, int VEC, int CP, bool CL> Kernel scan_kernel_c(bool gate, int q) {
-    return q == 1 ? scan_kernel_q<T, VEC, CP, 1, CL>(gate)
-         : q == 2 ? scan_kernel_q<T, VEC, CP, 2, CL>(gate)
-                  : scan_kernel_q<T, VEC, CP, 4, CL>(gate);
+template <typename T, int VEC, int CP, bool CL> Kernel scan_kernel_q(bool gate, int q) {
+    return q == 1 ? scan_kernel_w<T, VEC, CP, 1, CL, 4>(gate)
+         : q == 2 ? scan_kernel_w<T, VEC, CP, 2, CL, 4>(gate)
+                  : scan_kernel_w<T, VEC, CP, 4, CL, 4>(gate);
 }
-template <typename T, int VEC, int CP> Kernel scan_kernel(bool gate, int q, int cs) {
-    return cs > 1 ? scan_kernel_c<T, VEC, CP, true>(gate, q) : scan_kernel_c<T, VEC, CP, false>(gate, q);
+template <typename T, int VEC, int CP> Kernel scan_kernel(bool gate, const Cut &cut, int sms) {
+    // Two of 8 warps fit an SM as four of 4 do, and take half the rounds: 8192
+    // channels, 4096 rows 57 us for 61.  Not for fp32, whose rows are as long in
+    // bytes at half the channels (4096 x 4096: 48 for 44), nor where more than two
+    // CTAs come to an SM (13 x 4096 x 2048: 177 for 170).
+    if constexpr (VEC == 2)
+        if (cut.cs == 1 && cut.q == 2 && cut.units <= 2 * sms) return scan_kernel_w<T, VEC, CP, 2, false, 8>(gate);
+    return cut.cs > 1 ? scan_kernel_q<T, VEC, CP, true>(gate, cut.q) : scan_kernel_q<T, VEC, CP, false>(gate, cut.q);
 }
 
 jamba_ssm_status launch_scan(jssm::GatedArgs &a, int32_t dtype, const DeviceInfo *dev, void *stream) {
@@ -183,12 +191,13 @@ jamba_ssm_status launch_scan(jssm::GatedArgs &a, int32_t dtype, const DeviceInfo
     const int width = bf && cp >= 4 ? 64 : 32;  // channels of a warp's row
     const Cut cut = choose_cut(a, bf ? 2 : 4, dev->sms, Pass{4, 1.4, gate ? 4 : 3},
                                [&](int q) { return int64_t(a.d + width / q - 1) / (width / q); });
-    int q = cut.q, cs = cut.cs;
+    int cs = cut.cs;
     void *args[] = {&a, &cs};
-    const Kernel k = !bf ? (cp == 16 ? scan_kernel<float, 1, 16>(gate, q, cs) : scan_kernel<float, 1, 4>(gate, q, cs))
-                     : cp == 16 ? scan_kernel<Bf, 2, 16>(gate, q, cs)
-                     : cp == 4  ? scan_kernel<Bf, 2, 4>(gate, q, cs)
-                                : scan_kernel<Bf, 1, 2>(gate, q, cs);
+    const Kernel k = !bf ? (cp == 16 ? scan_kernel<float, 1, 16>(gate, cut, dev->sms)
+                                   : scan_kernel<float, 1, 4>(gate, cut, dev->sms))
+                     : cp == 16 ? scan_kernel<Bf, 2, 16>(gate, cut, dev->sms)
+                     : cp == 4  ? scan_kernel<Bf, 2, 4>(gate, cut, dev->sms)
+                                : scan_kernel<Bf, 1, 2>(gate, cut, dev->sms);
     return launch_clusters(k, cut.units, cs, args, dev, stream);
 }
 

@@ -54,7 +54,8 @@ def test_scan_matches_recurrence(dtype, batch, seqlen, d):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
-@pytest.mark.parametrize("batch,seqlen,d", [(40, 150, 512), (24, 300, 320), (2, 700, 2048)])
+@pytest.mark.parametrize("batch,seqlen,d", [(40, 150, 512), (24, 300, 320), (24, 150, 310),
+                                             (2, 700, 2048)])
 def test_scan_of_many_tiles(dtype, batch, seqlen, d):
     """Enough channel tiles for the whole device: the cuts without clusters."""
     x, g, z, rate, bias = _inputs((batch, seqlen, d), dtype, d)
@@ -284,6 +285,22 @@ def test_backward_matches_formulas(dtype, batch, seqlen, d, gate):
             continue
         assert_within(with_ck[k], v, e, k)
         assert torch.equal(with_ck[k], without[k]), f"{k} depends on who made the checkpoints"
+
+
+@pytest.mark.parametrize("dtype,batch,seqlen,d", [(BF, 24, 300, 320), (BF, 40, 100, 520),
+                                                  (F32, 24, 150, 310)])
+def test_backward_of_many_tiles(dtype, batch, seqlen, d):
+    """The cuts without clusters, from the forward's checkpoints."""
+    x, g, z, rate, bias = _inputs((batch, seqlen, d), dtype, d)
+    dev = x.device
+    h0, dh = torch.randn(batch, d, device=dev), torch.randn(batch, d, device=dev)
+    dout = torch.randn(batch, seqlen, d, device=dev).to(dtype)
+    ckpt = jamba_ssm_gated_scan_ckpt(x)
+    jamba_ssm_gated_scan(x, g, z=z, rate=rate, bias=bias, h0=h0, ckpt=ckpt)
+    got = jamba_ssm_gated_scan_bwd(x, g, dout, z=z, rate=rate, bias=bias, h0=h0, dh_final=dh,
+                                   ckpt=ckpt)
+    for k, (v, e) in Reference(x, g, z, rate, bias, h0).gradients(dout, dh).items():
+        assert_within(got[k], v, e, k)
 
 
 @pytest.mark.parametrize("dtype,d", [(BF, 50), (F32, 33), (BF, 64)])

@@ -149,6 +149,10 @@ def test_proj_empty_leading_shapes_and_out():
     assert out.shape == (2, 3, 20) and out.dtype == BF
     flat = jamba_ssm_i8_proj(q.view(6, 64), s.view(6), w, ws)
     assert torch.equal(out.view(6, 20), flat)
+    q1, s1 = jamba_ssm_i8_quant(x[1, 2])  # one row, without leading dimensions
+    assert q1.shape == (64,) and s1.shape == ()
+    one = jamba_ssm_i8_proj(q1, s1, w, ws)
+    assert one.shape == (20,) and torch.equal(one, out[1, 2])
     q0, s0 = jamba_ssm_i8_quant(x[:0])
     assert jamba_ssm_i8_proj(q0, s0, w, ws).shape == (0, 3, 20)
 
