@@ -59,7 +59,8 @@ jamba_ssm_status jamba_ssm_i8_quant(const jamba_ssm_i8_quant_params *p, void *st
 /*
  * out[t, o] = (sum_k q[t, k] w[o, k]) * q_scale[t] * w_scale[o] + bias[o]
  * The sum is exact (32-bit integers); the rest is fp32, rounded once to
- * out_dtype.
+ * out_dtype.  A token's outputs have the same bits whatever the other tokens of
+ * the call and their number are.
  *   q        [ntok, pitch] int8, w [n_out, pitch] int8, pitch =
  *            JAMBA_SSM_I8_PITCH(k); both 16-byte aligned; the columns behind k
  *            must be zero in one of the two at least.

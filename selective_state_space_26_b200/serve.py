@@ -64,7 +64,8 @@ def jamba_ssm_i8_quant(x, q=None, scale=None, stream=None):
 def jamba_ssm_i8_proj(q, q_scale, w, w_scale, bias=None, out=None, out_dtype=torch.bfloat16,
                       timeout_cycles: int = 0, stream=None, debug_flags: int = 0):
     """out = (q . w) * q_scale * w_scale + bias, the sum exact in 32-bit
-    integers, rounded once to out_dtype (bf16 or fp32).
+    integers, rounded once to out_dtype (bf16 or fp32).  A token's outputs have
+    the same bits whatever batch it is in.
 
     q int8 [..., pitch] and q_scale fp32 [...] of jamba_ssm_i8_quant; w int8
     [n_out, pitch] and w_scale fp32 [n_out] of the same call on the weight; bias

@@ -422,6 +422,37 @@ def test_updates_continue_a_scan():
     assert_within(state, ref.h_final, ref.e_final, "last state")
 
 
+def test_offsets_past_32_bits():
+    """2.2e9 elements in each activation and 2.2e9 in the state cache: the far end
+    is that of the same rows taken alone."""
+    dev, rows, d, cut = _dev(), 270_000, 8192, 269_000
+    gen = torch.Generator(device=dev)
+    gen.manual_seed(1)
+    x = torch.randn(1, rows, d, generator=gen, device=dev, dtype=BF)
+    g = torch.randn(1, rows, d, generator=gen, device=dev, dtype=BF)
+    out, hf = jamba_ssm_gated_scan(x, g)
+    _, h = jamba_ssm_gated_scan(x[:, :cut], g[:, :cut])
+    tail, ht = jamba_ssm_gated_scan(x[:, cut:], g[:, cut:], h0=h)
+    # both are within the recurrence's bound, 2^-21 of the largest |x| for each of the
+    # about 10 steps that a gate near 1/2 remembers, and half a bf16 step
+    assert ((tail - out[:, cut:]).abs().float() <= 2.0 ** -7 * tail.abs().float() + 1e-3).all()
+    assert (ht - hf).abs().max() < 1e-3
+    dout = torch.ones_like(x)
+    grads = jamba_ssm_gated_scan_bwd(x, g, dout)
+    part = jamba_ssm_gated_scan_bwd(x[:, cut:], g[:, cut:], dout[:, cut:], h0=h)
+    for k in ("dx", "dg"):
+        a, b = grads[k][:, cut:].float(), part[k].float()
+        assert ((a - b).abs() <= 2.0 ** -6 * b.abs() + 1e-3).all(), k
+    del out, tail, grads, part, dout
+    big = torch.zeros(270_000, 8192, device=dev)
+    idx = torch.tensor([269_999, 3], dtype=torch.int32, device=dev)
+    y = jamba_ssm_gated_state_update(big, x[0, :2], g[0, :2], state_indices=idx)
+    small = torch.zeros(2, 8192, device=dev)
+    want = jamba_ssm_gated_state_update(small, x[0, :2], g[0, :2])
+    assert torch.equal(y, want) and torch.equal(big[idx.long()], small)
+    assert int(torch.count_nonzero(big[4:269_999])) == 0
+
+
 def test_graph_streams_and_two_calls_at_once():
     """Captured and replayed on new inputs, beside an eager call on another
     stream: the two share nothing."""

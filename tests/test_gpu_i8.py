@@ -171,6 +171,44 @@ def test_quantised_linear_is_near_the_float_one():
     assert ((out - xd @ wd.T).abs() <= bound * (1 + 1e-5)).all()
 
 
+@pytest.mark.parametrize("k,n", [(64, 2048), (1000, 1027), (4096, 512)])
+@pytest.mark.parametrize("dtype", [BF, torch.float32])
+def test_tokens_do_not_depend_on_their_batch(k, n, dtype):
+    """Other token counts take other tiles and other splits of K; the sums are of
+    integers and the scales' order is fixed, so every bit stays."""
+    g = _gen(12)
+    m = 2305
+    q, s = jamba_ssm_i8_quant(torch.randn(m, k, generator=g, device="cuda"))
+    w, ws = jamba_ssm_i8_quant(torch.randn(n, k, generator=g, device="cuda"))
+    # scales of every size, some outside of what the fast order of the factors takes
+    s[::7] *= 2.0 ** 62
+    s[3::11] *= 2.0 ** -70
+    s[5::13] = 0.0
+    ws[::5] *= 2.0 ** -64
+    bias = torch.randn(n, generator=g, device="cuda")
+    out = jamba_ssm_i8_proj(q, s, w, ws, bias=bias, out_dtype=dtype)
+    for a, b in [(0, 1), (2304, 2305), (255, 272), (17, 49), (1000, 1064), (250, 450), (5, 905)]:
+        assert torch.equal(out[a:b], jamba_ssm_i8_proj(q[a:b], s[a:b], w, ws, bias=bias,
+                                                       out_dtype=dtype)), (a, b)
+
+
+def test_offsets_past_32_bits():
+    """2.2e9 inputs and outputs: the last rows are those of the same tokens alone."""
+    g = _gen(11)
+    m, k, n = 140_000, 15_984, 16_000
+    x = torch.randn(m, k, generator=g, device="cuda", dtype=BF)
+    q, s = jamba_ssm_i8_quant(x)
+    qt, st = jamba_ssm_i8_quant(x[-300:])
+    assert torch.equal(q[-300:], qt) and torch.equal(s[-300:], st)
+    del x
+    w, ws = jamba_ssm_i8_quant(torch.randn(n, 64, generator=g, device="cuda"))
+    thin = q[:, :64].contiguous()
+    out = jamba_ssm_i8_proj(thin, s, w, ws)
+    assert torch.equal(out[-300:], jamba_ssm_i8_proj(thin[-300:], s[-300:], w, ws))
+    assert torch.equal(out[:300], jamba_ssm_i8_proj(thin[:300], s[:300], w, ws))
+    assert jamba_ssm_serve_get_status() == 0
+
+
 def test_graph_and_streams():
     g = _gen(9)
     x = torch.randn(300, 1000, generator=g, device="cuda").to(BF)
