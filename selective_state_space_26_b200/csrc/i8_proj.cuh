@@ -82,6 +82,8 @@ __device__ __forceinline__ void i8_put(T *out, int64_t n, const uint32_t (&v)[CO
     const bool whole = __all_sync(0xffffffffu, on && cols >= COLS);
     if (tame && whole)
         i8_columns<T, true, true>(out, n, v, sc, w, bias, on, cols, pairs);
+    else if (tame)
+        i8_columns<T, true, false>(out, n, v, sc, w, bias, on, cols, pairs);
     else
         i8_columns<T, false, false>(out, n, v, sc, w, bias, on, cols, pairs);
 }
@@ -403,9 +405,13 @@ __global__ void __launch_bounds__(I8SplitCfg<NT>::kThreads, 1)
     }
     after_earlier_work();
     let_next_begin();
-    for (int i = threadIdx.x; i < NT; i += C::kThreads) scales[i] = m0 + i < a.ntok ? a.qs[m0 + i] : 0.0f;
+    bool tame = true;
+    for (int i = threadIdx.x; i < NT; i += C::kThreads) {
+        scales[i] = m0 + i < a.ntok ? a.qs[m0 + i] : 0.0f;
+        tame = tame && i8_tame(scales[i]);
+    }
     tc_fence_before();
-    __syncthreads();
+    tame = __syncthreads_and(tame);  // and the scales are staged
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(tmem_slot);
 
@@ -460,7 +466,7 @@ __global__ void __launch_bounds__(I8SplitCfg<NT>::kThreads, 1)
                 tmem_ld16_async(lanes + c, v);
                 tmem_wait_ld();
                 tmem_regs_ready(v);
-                i8_put<T>(out + int64_t(c) * a.n, a.n, v, scales + c, w, bias, on, cols - c, false, a.pairs);
+                i8_put<T>(out + int64_t(c) * a.n, a.n, v, scales + c, w, bias, on, cols - c, tame, a.pairs);
             }
         }
     } else {
@@ -509,7 +515,7 @@ __global__ void __launch_bounds__(I8SplitCfg<NT>::kThreads, 1)
                     }
                     mine += a.ks * C::kM;
                     const uint32_t acc[4] = {uint32_t(t.x), uint32_t(t.y), uint32_t(t.z), uint32_t(t.w)};
-                    i8_put<T>(out + int64_t(c) * a.n, a.n, acc, scales + c, w, bias, on, end - c, false,
+                    i8_put<T>(out + int64_t(c) * a.n, a.n, acc, scales + c, w, bias, on, end - c, tame,
                               a.pairs);
                 }
             } else {
@@ -520,7 +526,7 @@ __global__ void __launch_bounds__(I8SplitCfg<NT>::kThreads, 1)
                     t.x += p.x, t.y += p.y;
                 }
                 const uint32_t acc[2] = {uint32_t(t.x), uint32_t(t.y)};
-                i8_put<T>(out + int64_t(c0) * a.n, a.n, acc, scales + c0, w, bias, on, end - c0, false, a.pairs);
+                i8_put<T>(out + int64_t(c0) * a.n, a.n, acc, scales + c0, w, bias, on, end - c0, tame, a.pairs);
             }
         }
     }
