@@ -98,7 +98,8 @@ jamba_ssm_status jamba_ssm_i8_proj(const jamba_ssm_i8_proj_params *p, void *stre
  *   n[b]           the tokens that fit: new_lens cut where the batch reaches
  *                  max_tokens (the requests behind get fewer or none).
  *   cu_seqlens     [requests + 1]: their running sum, for the packed scans.
- *   positions      [max_tokens]: ctx_lens[b] + the token's place in n[b].
+ *   positions      [max_tokens]: ctx_lens[b] + the token's place in n[b], or
+ *                  -1 where that is 2^31 or more (the token has no block then).
  *   token_request  [max_tokens]: b.
  *   block_tables   [requests, max_blocks], read and written: the cache blocks
  *                  of block_size tokens that a request holds, in order.  The
@@ -122,10 +123,11 @@ jamba_ssm_status jamba_ssm_i8_proj(const jamba_ssm_i8_proj_params *p, void *stre
  * of max_tokens rows can run on fewer.
  * Recorded as JAMBA_SSM_ERR_INVALID_ARG in the status word: tokens past
  * max_tokens, blocks or slots past the free ones, a request longer than
- * max_blocks blocks.  The maps are then as said above.
+ * max_blocks blocks or with a position past 2^31 - 1.  The maps are then as
+ * said above.
  * requests in [0, 2^20], max_tokens in [0, 2^30], max_blocks in [1, 2^24],
  * block_size in [1, 2^20]; requests * max_blocks and the sums of lengths may
- * pass 2^31, a single request's ctx + new may not.
+ * pass 2^31.
  * free_blocks / free_slots may be NULL when their count is 0; ctx_lens NULL
  * means zeros.  All are device pointers, int32 unless said otherwise, aligned
  * to their element.  Outputs must not overlap one another or an input.

@@ -33,7 +33,9 @@ struct BatchMapsArgs {
 constexpr int kMapsThreads = 256, kMapsTokens = 4, kMapsFused = 2048;
 constexpr int kMapsManyThreads = 1024;
 
-__device__ __forceinline__ int ceil_div(int64_t v, int by) { return static_cast<int>((v + by - 1) / by); }
+constexpr int64_t kMapsPositions = int64_t(1) << 31;  // a position is an int32
+
+__device__ __forceinline__ int64_t ceil_div(int64_t v, int by) { return (v + by - 1) / by; }
 
 // One request's share, given n, the tokens of it that fit.
 struct MapsRequest {
@@ -46,10 +48,11 @@ __device__ __forceinline__ int maps_ctx(const BatchMapsArgs &a, int b) {
 __device__ __forceinline__ MapsRequest maps_request(const BatchMapsArgs &a, int ctx, int n) {
     MapsRequest r;
     r.ctx = ctx;
-    r.had = min(ceil_div(r.ctx, a.block_size), a.max_blocks);
-    const int need = n > 0 ? ceil_div(int64_t(r.ctx) + n, a.block_size) : r.had;
-    r.too_long = need > a.max_blocks;
-    r.take = max(min(need, a.max_blocks) - r.had, 0);
+    const int64_t most = a.max_blocks, end = int64_t(r.ctx) + n;
+    r.had = static_cast<int>(min(ceil_div(r.ctx, a.block_size), most));
+    const int64_t need = n > 0 ? ceil_div(min(end, kMapsPositions), a.block_size) : r.had;
+    r.too_long = need > most || (n > 0 && end > kMapsPositions);
+    r.take = max(static_cast<int>(min(need, most)) - r.had, 0);
     r.starts = n > 0 && r.ctx == 0;
     return r;
 }
@@ -131,7 +134,9 @@ __device__ __forceinline__ void maps_tokens(const BatchMapsArgs &a, const int *c
                 ctx = ctx_of(b);
             }
             req[i] = b;
-            pos[i] = ctx + static_cast<int>(t - cu[b]);
+            const int64_t p = ctx + (t - cu[b]);
+            if (p >= kMapsPositions) continue;  // no position: -1, as of a row without a token
+            pos[i] = static_cast<int>(p);
             const int j = pos[i] / a.block_size, in = pos[i] - j * a.block_size;
             if (j < a.max_blocks) {
                 const int blk = block_of(b, ctx, j, in);
@@ -213,7 +218,7 @@ template <int PER> __global__ void __launch_bounds__(kMapsThreads) batch_maps_ke
                 (int64_t(blockIdx.x) * kMapsThreads + threadIdx.x) * kMapsTokens,
                 [&](int b, int c, int j, int in) {
                     int32_t *entry = a.block_tables + int64_t(b) * a.max_blocks + j;
-                    const int fresh = j - ceil_div(c, a.block_size);
+                    const int64_t fresh = j - ceil_div(c, a.block_size);
                     if (fresh < 0) return *entry;
                     const int64_t f = int64_t(first[b]) + fresh;
                     const int blk = f < a.num_free_blocks ? a.free_blocks[f] : -1;

@@ -143,6 +143,56 @@ def test_many_requests_and_long_maps():
     assert not bad and _run(*args) == want
 
 
+@pytest.mark.parametrize("requests", [2, 2100])  # either form of the call
+@pytest.mark.parametrize("bs,width", [(16, 4), (1 << 20, 1 << 11), (1, 3)])
+def test_positions_past_31_bits(requests, bs, width):
+    """A context of 2^31 - 3 tokens has three positions left: the tokens behind
+    have none, touch no table and are recorded; the request behind is whole."""
+    ctx = _i32([2 ** 31 - 3, 0] + [5] * (requests - 2))
+    new = _i32([6, 2] + [0] * (requests - 2))
+    table = torch.full((requests, width), -7, dtype=torch.int32, device=ctx.device)
+    table[0] = torch.arange(width, device=ctx.device) + 100
+    maps = jamba_ssm_batch_maps(new, table, _i32([9, 8, 7]), _i32([-1] * requests), _i32([4]),
+                                ctx_lens=ctx, block_size=bs, max_tokens=16)
+    last = 2 ** 31 - 1
+    assert maps["positions"].tolist() == [last - 2, last - 1, last, -1, -1, -1, 0, 1] + [-1] * 8
+    assert maps["token_request"].tolist() == [0] * 6 + [1, 1] + [-1] * 8
+    there = [(100 + (last - i) // bs) * bs + (last - i) % bs if (last - i) // bs < width else -1
+             for i in (2, 1, 0)]
+    second = [9, 8] if bs == 1 else [9 * bs, 9 * bs + 1]
+    assert maps["slot_map"].tolist() == there + [-1] * 3 + second + [-1] * 8
+    assert table[0].tolist() == list(range(100, 100 + width))
+    taken = 2 if bs == 1 else 1
+    assert table[1, :3].tolist() == ([9, 8] if bs == 1 else [9]) + [-7] * (3 - taken)
+    assert maps["counts"].tolist() == [8, taken, 1, 6]
+    assert jamba_ssm_serve_get_status() == _lib.ERR_INVALID_ARG
+
+
+def test_tables_and_maps_past_32_bits():
+    """2.7e9 table entries and 2^30 rows of the per-token maps."""
+    requests, width, bs, rows = 160, 1 << 24, 16, 1 << 30
+    table = torch.full((requests, width), -3, dtype=torch.int32, device=_i32([0]).device)
+    new = [0] * requests
+    new[1], new[-1] = rows - 40, 40
+    blocks = -(-new[1] // bs) + 3
+    free = torch.arange(blocks, dtype=torch.int32, device="cuda") + 5
+    maps = jamba_ssm_batch_maps(_i32(new), table, free, _i32([-1] * requests), _i32([1, 0]),
+                                block_size=bs, max_tokens=rows)
+    # request 1 needs 2^26 blocks and has room for 2^24: recorded, the rest of it has no block
+    assert jamba_ssm_serve_get_status() == _lib.ERR_INVALID_ARG
+    assert maps["counts"].tolist() == [rows, width + 3, 2, rows - 40]
+    assert maps["positions"][-41:].tolist() == [rows - 41] + list(range(40))
+    assert maps["token_request"][-41:].tolist() == [1] + [requests - 1] * 40
+    mine = free[width:width + 3]
+    own = (mine.long()[:, None] * bs + torch.arange(bs, device="cuda")).flatten()[:40]
+    assert torch.equal(maps["slot_map"][-40:], own)
+    end = width * bs
+    assert maps["slot_map"][end - 2:end + 2].tolist() == [(width + 4) * bs + 14, (width + 4) * bs + 15, -1, -1]
+    assert torch.equal(table[-1, :4], torch.cat([mine, _i32([-3])]))
+    assert torch.equal(table[1], free[:width])
+    assert int((table[0] != -3).sum()) == 0 and int((table[2:-1] != -3).sum()) == 0
+
+
 def test_graph_replays_on_new_lengths():
     rng = random.Random(6)
     new, ctx, table, free, slots, free_slots, bs, _ = _case(rng, 40, 30, 16)
