@@ -285,6 +285,88 @@ template <typename T, int VEC, int S, int Q, int CP> struct GatedFeed {
         p += round;
     }
     __device__ __forceinline__ void skip() { p += round; }
+    // Where a lane finds row i of its run: behind first_word, in raw values.
+    static __device__ __forceinline__ int first_word(int lane) { return lane; }
+    __device__ __forceinline__ int word_of(int i) const { return i * 32; }
+};
+
+// The same where the rows begin at any multiple of 4 bytes (the array itself at 16):
+// 16-byte copies of the aligned bytes that hold a row's part, which is then read
+// from its place in them.  A lane copies the same part of every kRows-th row.  A run's
+// rows lie together, the runs apart so that their lanes' words fall into different
+// banks.  Bytes of neighbouring rows and channels come along unused; nothing before
+// the array is read, and behind it a copy is cut short.  A row of 64 bytes takes 5 of
+// an instruction's lanes in place of 16: 13 x 4096 x 1026 bf16 with z 135 us for 184.
+constexpr int kCpShifted = 0;
+template <typename T, int VEC, int S, int Q> struct GatedShiftedFeed {
+    static constexpr int kRow = 128 / Q;              // bytes of a row
+    static constexpr int kParts = kRow / 16 + 1;      // copies of a row
+    static constexpr int kRows = 32 / kParts;         // rows of one instruction
+    static constexpr int kPitch = kParts * 16;
+    static constexpr int kRun = S * kPitch + kRow % 128;
+    static constexpr int kBytes = Q * kRun;           // of an array's rows of one warp
+    static constexpr int kCopies = (S * Q + kRows - 1) / kRows;
+    static_assert(VEC * sizeof(T) == 4, "");
+    const char *p, *end;  // this lane's first row and its part of it (not rounded down), the array's end
+    const char *safe;  // from here on this lane's copies of a round may reach past the end
+    int64_t hop, round;
+    int word[4];  // of this lane in its run's rows i, i + 4, ...
+
+    static __device__ __forceinline__ int channel_of(int) { return 0; }
+    __device__ __forceinline__ void start(const void *base, int64_t row, int64_t rs, int c0, int lane,
+                                          int64_t stride, int64_t total, int d) {
+        constexpr int64_t es = sizeof(T);
+        const char *const b = static_cast<const char *>(base);
+        end = b + ((total - 1) * rs + d) * es;
+        p = b + ((row + lane / kParts) * rs + c0) * es + lane % kParts * 16;
+        hop = kRows * rs * es;
+        round = stride * rs * es;
+        safe = end - (kCopies - 1) * hop - 15;  // a copy ends at most 16 bytes behind its part's start
+        const int run = lane / (32 / Q), col = lane % (32 / Q);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {  // S and the strides are multiples of 4 rows
+            const int64_t at = ((row + i) * rs + c0) * es;
+            word[i] = run * (kRun / 4) + col + (static_cast<int>(at >> 2) & 3);
+        }
+    }
+    __device__ __forceinline__ void copy(uint32_t dst, bool, int n, int lane) {
+        const char *q = p;
+        const int first = lane / kParts;
+        dst += first * kPitch + lane % kParts * 16;
+        const bool on = first < kRows;
+        if (n == S * Q && p < safe) {
+#pragma unroll
+            for (int i = 0; i < kCopies; ++i) {
+                const int r = first + i * kRows;
+                if (on && r < S * Q) cp<16>(dst + i * (kRows * kPitch) + r / S * (kRun - S * kPitch), down(q));
+                q += hop;
+            }
+        } else if (on) {
+#pragma unroll 1
+            for (int r = first; r < n; r += kRows) {
+                const char *const from = down(q);
+                const int64_t left = end - from;
+                if (left > 0)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                                     dst + (r - first) * kPitch + r / S * (kRun - S * kPitch)),
+                                 "l"(from), "r"(static_cast<int>(min(left, int64_t(16))))
+                                 : "memory");
+                q += hop;
+            }
+        }
+        p += round;
+    }
+    static __device__ __forceinline__ const char *down(const char *q) {
+        return reinterpret_cast<const char *>(reinterpret_cast<uintptr_t>(q) & ~uintptr_t(15));
+    }
+    static __device__ __forceinline__ int first_word(int) { return 0; }
+    __device__ __forceinline__ int word_of(int i) const { return word[i & 3] + i * (kPitch / 4); }
+};
+template <typename T, int VEC, int S, int Q, int CP> struct GatedFeedOf {
+    using type = GatedFeed<T, VEC, S, Q, CP>;
+};
+template <typename T, int VEC, int S, int Q> struct GatedFeedOf<T, VEC, S, Q, kCpShifted> {
+    using type = GatedShiftedFeed<T, VEC, S, Q>;
 };
 
 __device__ __forceinline__ Lane1 lshfl_up(Lane1 a, int by) { return {__shfl_up_sync(~0u, a.v, by)}; }
@@ -329,10 +411,11 @@ __device__ __forceinline__ Lane2 lshfl_down(Lane2 a, int by) {
 constexpr int kGatedMaxCluster = 8;
 constexpr int kGatedRun = 16;
 
-template <bool GATE, int W> struct GatedScanCfg {
+template <bool GATE, int W, int Q, int CP> struct GatedScanCfg {
     static constexpr int kThreads = 32 * W;
     static constexpr int kArrays = GATE ? 3 : 2;
-    static constexpr int kArrayBytes = kGatedRun * 128;  // one array's rows of one warp
+    static constexpr int kArrayBytes =  // one array's rows of one warp
+        CP == kCpShifted ? GatedShiftedFeed<float, 1, kGatedRun, Q>::kBytes : kGatedRun * 128;
     static constexpr int kStageBytes = kArrays * kArrayBytes;
     static constexpr int kSmemBytes = W * 2 * kStageBytes;
 };
@@ -341,13 +424,13 @@ template <typename T, int VEC, bool GATE, int Q, int CP, bool CLUSTER, int W>
 __global__ void __launch_bounds__(32 * W, 16 / W) gated_scan_kernel(const GatedArgs a, int cs) {
     using Raw = GatedRaw<T, VEC>;
     using R = typename Raw::type;
-    using C = GatedScanCfg<GATE, W>;
+    using C = GatedScanCfg<GATE, W, Q, CP>;
     using L = Lane<VEC>;
     using Map = RunMap<VEC>;
     constexpr int S = kGatedRun, LPR = 32 / Q, kChunk = W * S * Q;
     constexpr int kBlockWarps = kGatedCkpt / (S * Q);  // warps of a checkpoint's 64 rows
     static_assert(kBlockWarps >= 1 && W % kBlockWarps == 0, "");
-    using F = GatedFeed<T, VEC, S, Q, CP>;
+    using F = typename GatedFeedOf<T, VEC, S, Q, CP>::type;
     extern __shared__ __align__(128) uint8_t stages[];
     __shared__ Map runs[2][W][LPR];
     __shared__ Map chunks[CLUSTER ? 2 : 1][CLUSTER ? kGatedMaxCluster : 1][LPR];
@@ -371,11 +454,17 @@ __global__ void __launch_bounds__(32 * W, 16 / W) gated_scan_kernel(const GatedA
     const int rounds = (len + stride - 1) / stride;
     int t = rank * kChunk + warp * (S * Q);  // this warp's first row
     uint8_t *const mine = stages + warp * (2 * C::kStageBytes);
-    const bool in = c0 + F::channel_of(lane) < a.d;
     F fg, fx, fz;
-    fg.start(a.g, row0 + t, a.gs, c0, lane, stride);
-    fx.start(a.x, row0 + t, a.xs, c0, lane, stride);
-    if (GATE) fz.start(a.z, row0 + t, a.zs, c0, lane, stride);
+    const bool in = c0 + F::channel_of(lane) < a.d;
+    if constexpr (CP == kCpShifted) {
+        fg.start(a.g, row0 + t, a.gs, c0, lane, stride, a.total, a.d);
+        fx.start(a.x, row0 + t, a.xs, c0, lane, stride, a.total, a.d);
+        if (GATE) fz.start(a.z, row0 + t, a.zs, c0, lane, stride, a.total, a.d);
+    } else {
+        fg.start(a.g, row0 + t, a.gs, c0, lane, stride);
+        fx.start(a.x, row0 + t, a.xs, c0, lane, stride);
+        if (GATE) fz.start(a.z, row0 + t, a.zs, c0, lane, stride);
+    }
     auto fill_gx = [&](int left, int stage) {  // left: rows from the copied round's first on
         if (left > 0) {
             const uint32_t to = smem_u32(mine) + stage * C::kStageBytes;
@@ -426,22 +515,25 @@ __global__ void __launch_bounds__(32 * W, 16 / W) gated_scan_kernel(const GatedA
         const bool full = len - t >= S * Q;
         const int n = min(len - t - run * S, S);  // rows of this lane's run
         const uint8_t *st = mine + par * C::kStageBytes;
-        const R *gr = reinterpret_cast<const R *>(st) + lane;
-        const R *xr = reinterpret_cast<const R *>(st + C::kArrayBytes) + lane;
-        const R *zr = reinterpret_cast<const R *>(st + 2 * C::kArrayBytes) + lane;
+        const R *gp = reinterpret_cast<const R *>(st) + F::first_word(lane);
+        const R *xp = reinterpret_cast<const R *>(st + C::kArrayBytes) + F::first_word(lane);
+        const R *zp = reinterpret_cast<const R *>(st + 2 * C::kArrayBytes) + F::first_word(lane);
+        auto gr = [&](int i) { return Raw::get(gp[fg.word_of(i)]); };
+        auto xr = [&](int i) { return Raw::get(xp[fx.word_of(i)]); };
+        auto zr = [&](int i) { return Raw::get(zp[fz.word_of(i)]); };
         oldest();  // this round's g and x
         // the states from zero and the products of (1 - u), row by row
         L h[S], P[S], ph = zero, pp = one;
         auto step = [&](int i, L s) {
             const L nu = lmul(s, nrate);
-            ph = lfma(nu, lsub(ph, Raw::get(xr[i * 32])), ph);
+            ph = lfma(nu, lsub(ph, xr(i)), ph);
             pp = lfma(nu, pp, pp);
         };
         bool good = full;
         if (full) {
 #pragma unroll
             for (int i = 0; i < S; ++i) {
-                step(i, lsigmoid_pair(ladd(Raw::get(gr[i * 32]), bias), good));
+                step(i, lsigmoid_pair(ladd(gr(i), bias), good));
                 h[i] = ph, P[i] = pp;
             }
         }
@@ -449,7 +541,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W) gated_scan_kernel(const GatedA
             ph = zero, pp = one;
 #pragma unroll
             for (int i = 0; i < S; ++i) {
-                if (i < n) step(i, lsigmoid(ladd(Raw::get(gr[i * 32]), bias)));
+                if (i < n) step(i, lsigmoid(ladd(gr(i), bias)));
                 h[i] = ph, P[i] = pp;
             }
         }
@@ -532,7 +624,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W) gated_scan_kernel(const GatedA
             for (int i = 0; i < S; ++i) {
                 L ov = lfma(P[i], mb, h[i]);
                 if (GATE) {
-                    const L zv = Raw::get(zr[i * 32]);
+                    const L zv = zr(i);
                     ov = lmul(ov, lmul(zv, lsigmoid_pair(zv, good)));
                 }
                 if (store) *reinterpret_cast<R *>(o) = Raw::put(ov);
@@ -545,7 +637,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W) gated_scan_kernel(const GatedA
             for (int i = 0; i < S; ++i) {
                 L ov = lfma(P[i], mb, h[i]);
                 if (GATE) {
-                    const L zv = Raw::get(zr[i * 32]);
+                    const L zv = zr(i);
                     ov = lmul(ov, lmul(zv, lsigmoid(zv)));
                 }
                 if (store && i < n) *reinterpret_cast<R *>(o) = Raw::put(ov);

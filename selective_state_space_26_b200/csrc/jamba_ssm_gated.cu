@@ -98,7 +98,8 @@ struct Cut {
 // the bytes (9 sequences, 3001 rows of 1000 fp32 channels, both passes: q 1 112,
 // q 2 66, q 4 52; 33 sequences, 16384 rows of 4096: q 1 94, q 2 113, q 4 160).
 struct Pass {
-    int per_sm;       // CTAs that fit an SM
+    int per_sm, per_sm4;  // CTAs that fit an SM, and of q = 4
+    int halves;           // half CTAs to an SM from which q = 2 takes no cluster
     double round_us;  // a round of one CTA
     int arrays;       // activations read and written
 };
@@ -109,7 +110,7 @@ Cut choose_cut(const jssm::GatedArgs &a, int es, int sms, const Pass &pass, Tile
         const int64_t units = batch * tiles(q), rows = int64_t(jssm::kGatedCkpt) * q;
         int cs = 1;
         while (cs < jssm::kGatedMaxCluster && cs * 2 <= (len + rows - 1) / rows &&
-               units * cs * 2 <= int64_t(pass.per_sm) * sms)
+               units * cs * 2 <= int64_t(q == 4 ? pass.per_sm4 : pass.per_sm) * sms)
             cs *= 2;
         return Cut{q, cs, units};
     };
@@ -119,12 +120,12 @@ Cut choose_cut(const jssm::GatedArgs &a, int es, int sms, const Pass &pass, Tile
         return !ragged || 3.0 * len / (jssm::kGatedCkpt * q) * pass.round_us <= all_us;
     };
     if (batch * tiles(1) >= 2 * sms && alone_ok(1)) return {1, 1, batch * tiles(1)};
-    if (batch * tiles(2) * 2 >= 3 * sms) {
+    if (batch * tiles(2) * 2 >= pass.halves * sms) {
         const int q = alone_ok(2) ? 2 : 4;
         return {q, 1, batch * tiles(q)};
     }
     const Cut two = clusters(2);
-    return two.units * two.cs * 2 < int64_t(pass.per_sm) * sms ? clusters(4) : two;
+    return two.units * two.cs * 2 < int64_t(pass.per_sm4) * sms ? clusters(4) : two;
 }
 
 using Bf = __nv_bfloat16;
@@ -163,12 +164,16 @@ jamba_ssm_status launch_clusters(const Kernel &k, int64_t units, int cs, void **
 }
 
 template <typename T, int VEC, int CP, int Q, bool CL, int W> Kernel scan_kernel_w(bool gate) {
-    using G = jssm::GatedScanCfg<true, W>;
-    using N = jssm::GatedScanCfg<false, W>;
-    return gate ? Kernel{(const void *)&jssm::gated_scan_kernel<T, VEC, true, Q, CP, CL, W>, G::kThreads,
-                         G::kSmemBytes}
-                : Kernel{(const void *)&jssm::gated_scan_kernel<T, VEC, false, Q, CP, CL, W>, N::kThreads,
-                         N::kSmemBytes};
+    using G = jssm::GatedScanCfg<true, W, Q, CP>;
+    using N = jssm::GatedScanCfg<false, W, Q, CP>;
+    if constexpr (CP == jssm::kCpShifted)  // with z only
+        return Kernel{(const void *)&jssm::gated_scan_kernel<T, VEC, true, Q, CP, CL, W>, G::kThreads,
+                      G::kSmemBytes};
+    else
+        return gate ? Kernel{(const void *)&jssm::gated_scan_kernel<T, VEC, true, Q, CP, CL, W>, G::kThreads,
+                             G::kSmemBytes}
+                    : Kernel{(const void *)&jssm::gated_scan_kernel<T, VEC, false, Q, CP, CL, W>, N::kThreads,
+                             N::kSmemBytes};
 }
 template <typename T, int VEC, int CP, bool CL> Kernel scan_kernel_q(bool gate, int q) {
     return q == 1 ? scan_kernel_w<T, VEC, CP, 1, CL, 4>(gate)
@@ -182,20 +187,36 @@ template <typename T, int VEC, int CP> Kernel scan_kernel(bool gate, const Cut &
     // CTAs come to an SM (13 x 4096 x 2048: 177 for 170).
     if constexpr (VEC == 2)
         if (cut.cs == 1 && cut.q == 2 && cut.units <= 2 * sms) return scan_kernel_w<T, VEC, CP, 2, false, 8>(gate);
-    return cut.cs > 1 ? scan_kernel_q<T, VEC, CP, true>(gate, cut.q) : scan_kernel_q<T, VEC, CP, false>(gate, cut.q);
+    if constexpr (VEC == 2 && CP == jssm::kCpShifted)  // without a cluster only
+        return scan_kernel_q<T, VEC, CP, false>(gate, cut.q);
+    else
+        return cut.cs > 1 ? scan_kernel_q<T, VEC, CP, true>(gate, cut.q) : scan_kernel_q<T, VEC, CP, false>(gate, cut.q);
 }
 
 jamba_ssm_status launch_scan(jssm::GatedArgs &a, int32_t dtype, const DeviceInfo *dev, void *stream) {
     const int cp = copy_bytes(a, dtype);
     const bool bf = dtype == JAMBA_SSM_BF16, gate = a.z != nullptr;
     const int width = bf && cp >= 4 ? 64 : 32;  // channels of a warp's row
-    const Cut cut = choose_cut(a, bf ? 2 : 4, dev->sms, Pass{4, 1.4, gate ? 4 : 3},
+    // Rows that begin at any multiple of 4 bytes, where three arrays are read: 16-byte
+    // copies of what holds them (us, 4-byte copies first: fp32 8 x 2048 x 4099 305
+    // and 231, 8192 x 515 43 and 28, 50001 x 1001 394 and 297; bf16 13 x 4096 x 1026
+    // 184 and 135).  Not for two arrays (50001 x 1001 fp32 182 and 195; 8192 x 514
+    // bf16 14 and 17) nor for bf16 in clusters (8192 x 2050 66 and 89).  Their stages
+    // are larger: three CTAs fit an SM, two of q = 4, and a cluster's barrier is
+    // hidden by fewer (8192 x 2501 x 2 fp32, q 2: one CTA to a tile 88, clusters of 4
+    // 120; 20001 x 1601: clusters of 2 233, of 4 158, of 8 209).
+    const bool any4 = cp == 4 && gate && aligned(a.x, 16) && aligned(a.g, 16) && aligned(a.z, 16);
+    const Pass pass = any4 && !bf ? Pass{3, 2, 2, 1.4, 4} : Pass{4, 4, 3, 1.4, gate ? 4 : 3};
+    const Cut cut = choose_cut(a, bf ? 2 : 4, dev->sms, pass,
                                [&](int q) { return int64_t(a.d + width / q - 1) / (width / q); });
+    const bool shifted = any4 && (!bf || cut.cs == 1);
     int cs = cut.cs;
     void *args[] = {&a, &cs};
     const Kernel k = !bf ? (cp == 16 ? scan_kernel<float, 1, 16>(gate, cut, dev->sms)
-                                   : scan_kernel<float, 1, 4>(gate, cut, dev->sms))
+                            : shifted ? scan_kernel<float, 1, jssm::kCpShifted>(gate, cut, dev->sms)
+                                      : scan_kernel<float, 1, 4>(gate, cut, dev->sms))
                      : cp == 16 ? scan_kernel<Bf, 2, 16>(gate, cut, dev->sms)
+                     : shifted  ? scan_kernel<Bf, 2, jssm::kCpShifted>(gate, cut, dev->sms)
                      : cp == 4  ? scan_kernel<Bf, 2, 4>(gate, cut, dev->sms)
                                 : scan_kernel<Bf, 1, 2>(gate, cut, dev->sms);
     return launch_clusters(k, cut.units, cs, args, dev, stream);
@@ -220,7 +241,7 @@ jamba_ssm_status launch_bwd(jssm::GatedArgs &a, int32_t dtype, const DeviceInfo 
     const int cp = copy_bytes(a, dtype);
     const bool bf = dtype == JAMBA_SSM_BF16, gate = a.z != nullptr;
     const int width = bf && cp >= 4 ? 64 : 32;
-    const Cut cut = choose_cut(a, bf ? 2 : 4, dev->sms, Pass{2, 2.4, gate ? 7 : 5},
+    const Cut cut = choose_cut(a, bf ? 2 : 4, dev->sms, Pass{2, 2, 3, 2.4, gate ? 7 : 5},
                                [&](int q) { return int64_t(a.d + width / q - 1) / (width / q); });
     int q = cut.q, cs = cut.cs;
     void *args[] = {&a, &cs};

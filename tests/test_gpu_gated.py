@@ -114,6 +114,39 @@ def test_strided_rows(dtype, d):
     assert torch.equal(one, out[:, :1])
 
 
+@pytest.mark.parametrize("dtype,d,strides", [
+    (F32, 1, (1, 1, 1)), (F32, 2, (5, 2, 7)), (F32, 3, (3, 6, 3)), (F32, 31, (31, 33, 34)),
+    (F32, 33, (39, 33, 33)), (F32, 515, (515, 517, 518)), (F32, 130, (130, 130, 131)),
+    (BF, 2, (2, 2, 2)), (BF, 6, (6, 10, 8)), (BF, 62, (62, 64, 66)), (BF, 1026, (1026, 1028, 1030)),
+])
+@pytest.mark.parametrize("batch,seqlen", [(1, 1), (1, 130), (70, 97)])
+def test_rows_at_any_multiple_of_4_bytes(dtype, d, strides, batch, seqlen):
+    """x, g and z with their own row strides, in buffers whose every other byte is a
+    NaN: rows behind the last, channels past the width, and what lies between."""
+    dev, rows = _dev(), batch * seqlen
+    gen = torch.Generator(device=dev)
+    gen.manual_seed(d)
+    views = []
+    for s in strides:
+        buf = torch.full(((rows + 2) * s + d,), float("nan"), device=dev, dtype=dtype)
+        v = buf.as_strided((batch, seqlen, d), (seqlen * s, s, 1))
+        v.copy_(torch.randn(batch, seqlen, d, generator=gen, device=dev))
+        views.append(v)
+    x, g, z = views
+    h0 = torch.randn(batch, d, generator=gen, device=dev)
+    out, hf = jamba_ssm_gated_scan(x, g, z=z, h0=h0)
+    _check_scan(Reference(x, g, z, h0=h0), out, hf, f"{dtype} {d} {strides}")
+    # the same rows as packed sequences of other lengths
+    cu = sorted({0, rows // 3, rows // 2, rows})
+    px, pg, pz = (v.as_strided((rows, d), (s, 1)) for v, s in zip(views, strides))
+    out, hf = jamba_ssm_gated_scan(px, pg, z=pz,
+                                   cu_seqlens=torch.tensor(cu, dtype=torch.int32, device=dev))
+    for i, (lo, hi) in enumerate(zip(cu, cu[1:])):
+        ref = Reference(px[None, lo:hi], pg[None, lo:hi], pz[None, lo:hi])
+        assert_within(out[lo:hi][None], ref.out, ref.e_out, f"sequence {i}")
+        assert_within(hf[i:i + 1], ref.h_final, ref.e_final, f"state {i}")
+
+
 LENGTHS = [0, 1, 63, 64, 65, 700, 0, 17, 128, 2]
 
 
