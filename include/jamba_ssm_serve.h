@@ -69,9 +69,11 @@ jamba_ssm_status jamba_ssm_i8_quant(const jamba_ssm_i8_quant_params *p, void *st
  * ntok in [0, 2^31 - 2^16], n_out in [1, 2^24], k in [1, JAMBA_SSM_I8_MAX_K].
  * timeout_cycles: limit of the kernel's waits in SM clock cycles (0 = about
  * 2 s); a wait that ran out is recorded as JAMBA_SSM_ERR_TIMEOUT, and the
- * outputs are not all written then.  debug_flags: 0 in production; bit 0
- * withholds every CTA's first copies, so that its waits run out (the test of
- * that path).
+ * outputs are not all written then: those that depend on the lost copies stay
+ * as they were, and none is written with a part of its sum.  debug_flags: 0 in
+ * production; bit 0 withholds every CTA's first copies, so that its waits run
+ * out, bit 1 those of the first of the CTAs that share a tile's K (the tests
+ * of that path).
  */
 typedef struct jamba_ssm_i8_proj_params {
     size_t struct_size;              /* = sizeof(jamba_ssm_i8_proj_params) */

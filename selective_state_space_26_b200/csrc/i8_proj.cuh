@@ -21,7 +21,7 @@ struct I8ProjArgs {
     int ntok, n, kblocks;  // kblocks: 128-byte blocks of K
     int ks;                // CTAs that share a tile's K (the split kernel)
     bool pairs;            // two bf16 channels can be written as a word
-    bool withhold;         // test of the bounded waits: leave out the first copies
+    uint32_t withhold;     // test of the bounded waits: ranks (bits) that leave out their first copies
     uint64_t limit;
 };
 
@@ -255,7 +255,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(I8PairCfg::kThreads,
                         ok = false;
                         break;
                     }
-                    if (a.withhold && wi == 0) continue;
+                    if (wi == 0 && ((a.withhold >> rank) & 1u)) continue;
                     uint8_t *st = smem + s * C::kStage;
                     if (leader) mbar_arrive_expect_tx(&full[s], 2 * C::kStage);
                     const uint32_t bar = mapa(smem_u32(&full[s]), 0);
@@ -378,6 +378,7 @@ __global__ void __launch_bounds__(I8SplitCfg<NT>::kThreads, 1)
     uint64_t *empty = full + C::kStages, *acc_full = empty + C::kStages;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_full + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    volatile int *sums_lost = abort_flag + 1;  // another CTA of the cluster gave a wait up
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = a.ks > 1 ? static_cast<int>(cta_rank()) : 0;
     const I8Wait wait{a.limit, abort_flag};
@@ -394,7 +395,7 @@ __global__ void __launch_bounds__(I8SplitCfg<NT>::kThreads, 1)
             mbar_init(&empty[s], 1);
         }
         mbar_init(acc_full, 1);
-        *abort_flag = 0;
+        *abort_flag = *sums_lost = 0;
         fence_mbarrier_init();
         prefetch_tensormap(&map_w);
         prefetch_tensormap(&map_q);
@@ -421,7 +422,7 @@ __global__ void __launch_bounds__(I8SplitCfg<NT>::kThreads, 1)
             for (; issued < cnt; ++issued) {
                 const int s = issued % C::kStages;
                 if (issued >= C::kStages && !wait(&empty[s], ((issued / C::kStages) & 1) ^ 1)) break;
-                if (a.withhold && issued == 0) continue;
+                if (issued == 0 && ((a.withhold >> rank) & 1u)) continue;
                 uint8_t *st = smem + s * C::kStage;
                 mbar_arrive_expect_tx(&full[s], C::kStage);
                 tma_load_2d(st, &map_w, (kb0 + issued) * 128, n0, &full[s]);
@@ -453,7 +454,7 @@ __global__ void __launch_bounds__(I8SplitCfg<NT>::kThreads, 1)
     tc_fence_after();
     const int q = warp & 3;
     const int o = n0 + q * 32 + lane;
-    const bool on = o < a.n && !*abort_flag;
+    bool on = o < a.n && !*abort_flag;
     const float w = on ? a.ws[o] : 0.0f, bias = on && a.bias ? a.bias[o] : 0.0f;
     const int cols = min(NT, a.ntok - m0);
     T *out = static_cast<T *>(a.out) + int64_t(m0) * a.n + o;
@@ -475,6 +476,12 @@ __global__ void __launch_bounds__(I8SplitCfg<NT>::kThreads, 1)
         uint8_t *sums = smem;
         const int own = NT / a.ks, log_own = __ffs(own) - 1;
         cluster_barrier();  // every CTA's stages are free
+        if (threadIdx.x < a.ks && *abort_flag)  // no CTA takes this one's part for a sum
+            asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(
+                             mapa(smem_u32(const_cast<int *>(sums_lost)), threadIdx.x)),
+                         "r"(1)
+                         : "memory");
+        __syncwarp();
         if (warp >= 2) {
             const int width = own >= 4 ? 4 : 2;  // columns of a group
             const uint32_t at = smem_u32(sums) + (rank * C::kM + q * 32 + lane) * width * 4;
@@ -503,6 +510,7 @@ __global__ void __launch_bounds__(I8SplitCfg<NT>::kThreads, 1)
             }
         }
         cluster_barrier();
+        on = on && !*sums_lost;
         if (warp >= 2) {
             const int c0 = rank * own, end = min(c0 + own, cols);
             if (own >= 4) {

@@ -210,7 +210,7 @@ JSSM_SERVE_API jamba_ssm_status jamba_ssm_i8_proj(const jamba_ssm_i8_proj_params
     a.n = static_cast<int>(p.n_out);
     a.kblocks = static_cast<int>(ceil_div(pitch, 128));
     a.limit = p.timeout_cycles ? p.timeout_cycles : kDefaultTimeoutCycles;
-    a.withhold = (p.debug_flags & 1u) != 0;
+    a.withhold = (p.debug_flags & 1u) ? 0xffu : 0u;
     const bool bf = p.out_dtype == JAMBA_SSM_BF16;
     a.pairs = bf && p.n_out % 2 == 0 && aligned(p.out, 4);
     CUtensorMap map_w, map_q;
@@ -229,6 +229,7 @@ JSSM_SERVE_API jamba_ssm_status jamba_ssm_i8_proj(const jamba_ssm_i8_proj_params
     } else {
         if (!encode_bytes(fn, &map_q, p.q, pitch, p.ntok, cut.nt)) return cuda_fail(cudaErrorInvalidValue);
         k = bf ? split_kernel<__nv_bfloat16>(cut.nt) : split_kernel<float>(cut.nt);
+        if (p.debug_flags & 2u) a.withhold |= 1u;
         grid = cut.tiles * cut.ks;
         if (grid > 0x7fffffff) return JAMBA_SSM_ERR_UNSUPPORTED;
     }

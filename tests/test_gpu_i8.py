@@ -252,6 +252,24 @@ def test_waits_that_run_out_are_reported(m, k, n):
     assert jamba_ssm_serve_get_status() == 0
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("m,k,n", [(8, 8192, 4096), (3, 4096, 300), (64, 8192, 1024)])
+def test_no_part_of_a_sum_is_written(m, k, n, dtype):
+    """One of the CTAs that share a tile's K gives its waits up: the others, whose
+    copies all arrived, write nothing of that tile either."""
+    g = _gen(4)
+    q, s = jamba_ssm_i8_quant(torch.randn(m, k, generator=g, device="cuda"))
+    w, ws = jamba_ssm_i8_quant(torch.randn(n, k, generator=g, device="cuda"))
+    good = jamba_ssm_i8_proj(q, s, w, ws, out_dtype=dtype)
+    out = torch.full_like(good, 12345.0)
+    jamba_ssm_i8_proj(q, s, w, ws, out=out, timeout_cycles=2_000_000, debug_flags=2)
+    assert jamba_ssm_serve_get_status() == _lib.ERR_TIMEOUT
+    assert ((out == torch.full_like(out, 12345.0)) | (out == good)).all()
+    assert not torch.equal(out, good)
+    assert torch.equal(jamba_ssm_i8_proj(q, s, w, ws, out_dtype=dtype), good)
+    assert jamba_ssm_serve_get_status() == 0
+
+
 def test_refusals():
     g = _gen(1)
     q, s = jamba_ssm_i8_quant(torch.randn(4, 32, generator=g, device="cuda"))
