@@ -83,6 +83,12 @@ def cuda_device(t, name, what):
     return t.device
 
 
+def _device_of(stream):
+    """The device of a stream that says it (None: a raw handle)."""
+    dev = getattr(stream, "device", None)
+    return dev if isinstance(dev, torch.device) else None
+
+
 def launching(stream, device):
     """Context for a call's allocations and launch: the tensors' device is the
     current one and, where the caller names a stream, that stream too, so what
@@ -94,6 +100,15 @@ def launching(stream, device):
         stream = torch.cuda.ExternalStream(raw, device=device) if raw else \
             torch.cuda.default_stream(device)
     return torch.cuda.stream(stream)
+
+
+def status_device(stream, device, workspace=None):
+    """The device, with its index, of a status word: of the named one, the
+    workspace or the stream, the first that is given, else the current one."""
+    dev = device if device is not None else workspace.device if workspace is not None else \
+        _device_of(stream)
+    dev = torch.device("cuda" if dev is None else dev)
+    return dev if dev.index is not None else torch.device(dev.type, torch.cuda.current_device())
 
 
 def raw_stream(device):

@@ -16,7 +16,7 @@ import torch
 from . import _lib
 from ._lib import JambaSSMError
 from ._tensors import (IO, check, cuda_device, empty_like, launching, need, ptr,
-                       raw_stream, row_stride)
+                       raw_stream, row_stride, status_device)
 from ._tensors import workspace as _workspace
 
 __all__ = ["jamba_ssm_gated_scan", "jamba_ssm_gated_scan_ckpt", "jamba_ssm_gated_scan_ckpt_size",
@@ -218,8 +218,7 @@ def jamba_ssm_gated_state_update(state, x, g, z=None, rate=None, bias=None, out=
 def jamba_ssm_gated_get_status(stream=None, device=None, workspace=None) -> int:
     """Wait for the stream, then read and clear a status word: the workspace's,
     or the device's word of this library when none is given."""
-    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else \
-        torch.device(device)
-    ws, _ = _workspace(workspace, workspace.device if workspace is not None else dev)
+    dev = status_device(stream, device, workspace)
+    ws, _ = _workspace(workspace, dev)
     with launching(stream, dev):
         return _lib.gated_lib().jamba_ssm_gated_get_status(ws, raw_stream(dev))

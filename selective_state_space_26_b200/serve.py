@@ -17,7 +17,8 @@ import torch
 
 from . import _lib
 from ._lib import JambaSSMError
-from ._tensors import IO, check, cuda_device, launching, need, ptr, raw_stream, row_stride
+from ._tensors import (IO, check, cuda_device, launching, need, ptr, raw_stream, row_stride,
+                       status_device)
 
 __all__ = ["jamba_ssm_i8_quant", "jamba_ssm_i8_proj", "jamba_ssm_batch_maps",
            "jamba_ssm_serve_get_status"]
@@ -166,7 +167,6 @@ def jamba_ssm_batch_maps(new_lens, block_tables, free_blocks, request_slots, fre
 
 def jamba_ssm_serve_get_status(stream=None, device=None) -> int:
     """Wait for the stream, then read and clear this library's status word."""
-    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else \
-        torch.device(device)
+    dev = status_device(stream, device)
     with launching(stream, dev):
         return _lib.serve_lib().jamba_ssm_serve_get_status(raw_stream(dev))

@@ -270,3 +270,61 @@ def test_python_calls_need_cuda_tensors():
                  lambda: jssm.jamba_ssm_batch_maps(i, i[None], i, i, i, max_tokens=2)):
         with pytest.raises(ValueError, match="no CPU path"):
             call()
+
+
+@pytest.fixture
+def two_devices(monkeypatch):
+    """The bindings as they are with devices 0 (current) and 1, and a library that
+    only writes down which stream it was given while which device was current."""
+    import contextlib
+
+    import torch
+    now, calls = [0], []
+
+    @contextlib.contextmanager
+    def current(dev):
+        now.append(torch.device(dev).index)
+        yield
+        now.pop()
+
+    class Lib:
+        def jamba_ssm_gated_get_status(self, ws, stream):
+            calls.append((now[-1], ws, stream))
+            return 0
+
+        def jamba_ssm_serve_get_status(self, stream):
+            calls.append((now[-1], None, stream))
+            return 0
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: now[-1])
+    monkeypatch.setattr(torch.cuda, "device", current)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: 0x100 + (0 | index))
+    monkeypatch.setattr(_lib, "gated_lib", Lib)
+    monkeypatch.setattr(_lib, "serve_lib", Lib)
+    return calls
+
+
+def test_status_of_a_device_without_an_index(two_devices):
+    import torch
+
+    import selective_state_space_26_b200 as jssm
+    for status in (jssm.jamba_ssm_gated_get_status, jssm.jamba_ssm_serve_get_status):
+        for device in (None, "cuda", torch.device("cuda"), "cuda:0", 0):
+            assert status(device=device) == 0
+            assert two_devices.pop() == (0, None, 0x100)
+        assert status(device="cuda:1") == 0
+        assert two_devices.pop() == (1, None, 0x101)
+
+
+def test_status_of_a_workspace_on_another_device(two_devices, monkeypatch):
+    """The stream that is waited for is one of the workspace's device."""
+    import torch
+
+    import selective_state_space_26_b200 as jssm
+    from selective_state_space_26_b200 import gated
+
+    class Words:
+        device = torch.device("cuda:1")
+    monkeypatch.setattr(gated, "_workspace", lambda ws, dev: (0x5000, 16))
+    assert jssm.jamba_ssm_gated_get_status(workspace=Words()) == 0
+    assert two_devices == [(1, 0x5000, 0x101)]

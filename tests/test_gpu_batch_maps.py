@@ -302,3 +302,11 @@ def test_serving_run():
         assert_within(y, ref.out, ref.e_out, f"request {b}")
         assert torch.equal(torch.cat([v[1] for v in outs[b]]), project(y, w_out, s_out))
         assert_within(cache[int(slots[b])], ref.h_final[0], ref.e_final[0], f"state {b}")
+
+
+def test_status_without_a_device_index():
+    from selective_state_space_26_b200 import jamba_ssm_gated_get_status
+    _i32([0])  # a device
+    for device in (None, "cuda", torch.device("cuda"), 0):
+        assert jamba_ssm_serve_get_status(device=device) == 0
+        assert jamba_ssm_gated_get_status(device=device) == 0
