@@ -95,6 +95,9 @@ def launching(stream, device):
     is allocated for the call belongs to the stream that uses it."""
     if stream is None:
         return _HERE if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+    # the kernel would run on the stream's device, with the tensors' addresses
+    if _device_of(stream) not in (None, device):
+        raise ValueError(f"stream is on {stream.device}, expected {device}")
     if not isinstance(stream, torch.cuda.Stream):
         raw = int(getattr(stream, "cuda_stream", stream))
         stream = torch.cuda.ExternalStream(raw, device=device) if raw else \

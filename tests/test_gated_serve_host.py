@@ -328,3 +328,21 @@ def test_status_of_a_workspace_on_another_device(two_devices, monkeypatch):
     monkeypatch.setattr(gated, "_workspace", lambda ws, dev: (0x5000, 16))
     assert jssm.jamba_ssm_gated_get_status(workspace=Words()) == 0
     assert two_devices == [(1, 0x5000, 0x101)]
+
+
+def test_stream_of_another_device_is_refused(two_devices):
+    """Before anything is enqueued: the kernel would run there, on this device's
+    addresses."""
+    from types import SimpleNamespace
+
+    import torch
+
+    import selective_state_space_26_b200 as jssm
+    from selective_state_space_26_b200 import _tensors
+    there = SimpleNamespace(cuda_stream=0x900, device=torch.device("cuda:1"))
+    with pytest.raises(ValueError, match="stream is on cuda:1, expected cuda:0"):
+        _tensors.launching(there, torch.device("cuda:0"))
+    for status in (jssm.jamba_ssm_gated_get_status, jssm.jamba_ssm_serve_get_status):
+        with pytest.raises(ValueError, match="stream is on cuda:1"):
+            status(stream=there, device=0)
+    assert two_devices == []
