@@ -184,8 +184,10 @@ template <typename T, int VEC, int CP> Kernel scan_kernel(bool gate, const Cut &
     // Two of 8 warps fit an SM as four of 4 do, and take half the rounds: 8192
     // channels, 4096 rows 57 us for 61.  Not for fp32, whose rows are as long in
     // bytes at half the channels (4096 x 4096: 48 for 44), nor where more than two
-    // CTAs come to an SM (13 x 4096 x 2048: 177 for 170).
-    if constexpr (VEC == 2)
+    // CTAs come to an SM (13 x 4096 x 2048: 177 for 170), nor for the shifted
+    // copies, whose stages leave room for one of 8 warps and three of 4 (4096 x
+    // 8194 110 for 100, 24 x 300 x 310 15.9 for 12.3).
+    if constexpr (VEC == 2 && CP != jssm::kCpShifted)
         if (cut.cs == 1 && cut.q == 2 && cut.units <= 2 * sms) return scan_kernel_w<T, VEC, CP, 2, false, 8>(gate);
     if constexpr (VEC == 2 && CP == jssm::kCpShifted)  // without a cluster only
         return scan_kernel_q<T, VEC, CP, false>(gate, cut.q);
