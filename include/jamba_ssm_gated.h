@@ -10,9 +10,11 @@
  *     u_t   = rate[d] * sigmoid(g_t + bias[d])           (update rate)
  *     h_t   = h_{t-1} + u_t (x_t - h_{t-1})              = (1 - u_t) h_{t-1} + u_t x_t
  *     out_t = h_t * silu(z_t),  silu(z) = z / (1 + e^-z)   (no z: out_t = h_t)
- * rate, in [0, 1], caps a channel's update rate and so sets how long it
- * remembers (about 1 / rate tokens).  The form h + u (x - h) never rounds the
- * decay 1 - u, so a rate of 1e-6 still moves the state by the right amount.
+ * rate, in [0, 1] (values are not checked), caps a channel's update rate and so
+ * sets how long it remembers (about 1 / rate tokens).  The form h + u (x - h)
+ * never rounds the decay 1 - u, and the scans join their runs of rows in the
+ * same form, so a rate of 1e-6 still moves the state by the right amount and
+ * leaves a state that has reached its input there.
  * A state that is not finite leaves every later step of its sequence not
  * finite.
  *

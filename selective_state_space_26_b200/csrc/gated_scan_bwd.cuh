@@ -6,8 +6,8 @@
 //   drate = sum du s,  dbias = sum dg.
 //
 // c runs backwards through the sequence as the state runs forwards: a run of
-// rows maps the c behind it to P c + R with the same P = prod(1 - u), and runs
-// compose.  So the kernel is the scan's with the order reversed: a lane takes a
+// rows maps the c behind it to P c + R with the same P = prod(1 - u), held as the
+// scan's maps hold it, and runs compose.  So the kernel is the scan's with the order reversed: a lane takes a
 // run of 8 rows, a warp Q runs, a CTA's 8 warps a chunk of 64 Q rows, a cluster
 // consecutive chunks, from the sequence's end to its start.  The states that du
 // and dz need come from the forward's checkpoints, one for every 64 rows, so
@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(kGatedBwdThreads, 2) gated_scan_bwd_kernel(con
         rate.set(v, on && a.rate ? a.rate[c + v] : 1.0f);
         bias.set(v, on && a.bias ? a.bias[c + v] : 0.0f);
     }
-    const L one = L::of(1.0f), zero = L::of(0.0f), nrate = lmul(rate, L::of(-1.0f));
+    const L one = L::of(1.0f), zero = L::of(0.0f), held = L::of(kHeld), nrate = lmul(rate, L::of(-1.0f));
     L drate = zero, dbias = zero;
     const float *ck = a.ckpt + (row0 / kGatedCkpt + b) * a.d + c;  // the sequence's first entry
     auto checkpoint = [&](int at) {  // the state before the 64 rows around row `at`
@@ -144,10 +144,11 @@ __global__ void __launch_bounds__(kGatedBwdThreads, 2) gated_scan_bwd_kernel(con
         // the run's maps: of the state, P h + hb, and of the gradient, P c + rb.  The
         // latter is a sum forwards too: row i's dy reaches the rows before the run
         // through the product of (1 - u) up to and with its own.
-        L s[S], dy[S], P = one, hb = zero, rb = zero;  // dy holds sigmoid(z) until z has been used
+        L s[S], dy[S], P = one, pn = zero, hb = zero, rb = zero;  // dy holds sigmoid(z) until z has been used
         auto ahead = [&](int i) {
             const L nu = lmul(s[i], nrate);
             hb = lfma(nu, lsub(hb, Raw::get(xr[i * 32])), hb);
+            pn = lfma(nu, P, pn);
             P = lfma(nu, P, P);
             L d = Raw::get(dr[i * 32]);
             if (GATE) d = lmul(d, lmul(Raw::get(zr[i * 32]), dy[i]));
@@ -163,7 +164,7 @@ __global__ void __launch_bounds__(kGatedBwdThreads, 2) gated_scan_bwd_kernel(con
             }
         }
         if (!good && on) {
-            P = one, hb = rb = zero;
+            P = one, pn = hb = rb = zero;
 #pragma unroll
             for (int i = 0; i < S; ++i) {
                 if (i < n) {
@@ -174,26 +175,27 @@ __global__ void __launch_bounds__(kGatedBwdThreads, 2) gated_scan_bwd_kernel(con
             }
         }
         // the warp's runs before and behind this one; P and both totals over the warp
-        L bp = one, bb = zero, ap = one, ab = zero, wp = P, wb = hb, wr = rb;
+        const L q = ldecay(P, pn);
+        L bp = held, bb = zero, ap = held, ab = zero, wp = q, wb = hb, wr = rb;
         if constexpr (Q > 1) {
-            L ip = P, ib = hb;
+            L ip = q, ib = hb;
 #pragma unroll
             for (int by = LPR; by < 32; by *= 2) {
                 const L op = lshfl_up(ip, by), ob = lshfl_up(ib, by);
                 if (lane >= by) {
-                    ib = lfma(ip, ob, ib);
-                    ip = lmul(ip, op);
+                    ib = lapply(ip, ob, ib);
+                    ip = ljoin(ip, op);
                 }
             }
             const L ep = lshfl_up(ip, LPR), eb = lshfl_up(ib, LPR);
             if (run > 0) bp = ep, bb = eb;
-            L jp = P, jr = rb;
+            L jp = q, jr = rb;
 #pragma unroll
             for (int by = LPR; by < 32; by *= 2) {
                 const L op = lshfl_down(jp, by), orr = lshfl_down(jr, by);
                 if (lane + by < 32) {
-                    jr = lfma(jp, orr, jr);
-                    jp = lmul(jp, op);
+                    jr = lapply(jp, orr, jr);
+                    jp = ljoin(jp, op);
                 }
             }
             const L fp = lshfl_down(jp, LPR), fr = lshfl_down(jr, LPR);
@@ -213,23 +215,23 @@ __global__ void __launch_bounds__(kGatedBwdThreads, 2) gated_scan_bwd_kernel(con
         for (int w = 0; w < W; ++w) maps[w] = runs[par][w][col], backs[w] = back[par][w][col];
 #pragma unroll
         for (int w = 0; w < W - 1; ++w)
-            if (w >= w0 && w < warp) h = lfma(maps[w].P(), h, maps[w].b());
-        h = lfma(bp, h, bb);
+            if (w >= w0 && w < warp) h = lapply(maps[w].q(), h, maps[w].b());
+        if (Q > 1) h = lapply(bp, h, bb);
         // c behind this warp's rows
         L cb;
         if constexpr (CLUSTER) {
-            L mp = one;
+            L mp = held;
             cb = zero;
 #pragma unroll
             for (int w = W - 1; w > 0; --w) {
                 if (w > warp) {
-                    cb = lfma(maps[w].P(), cb, backs[w]);
-                    mp = lmul(maps[w].P(), mp);
+                    cb = lapply(maps[w].q(), cb, backs[w]);
+                    mp = ljoin(maps[w].q(), mp);
                 }
             }
             if (warp == 0 && run == 0) {  // the chunk's map to every CTA of the cluster
-                const L p = maps[0].P();
-                const Map m = Map::of(lmul(p, mp), lfma(p, cb, wr));
+                const L p = maps[0].q();
+                const Map m = Map::of(ljoin(p, mp), lapply(p, cb, wr));
                 const uint32_t at = smem_u32(&chunks[par][rank][col]);
 #pragma unroll
                 for (int r = 0; r < kGatedMaxCluster; ++r)
@@ -244,19 +246,19 @@ __global__ void __launch_bounds__(kGatedBwdThreads, 2) gated_scan_bwd_kernel(con
                 if (r == rank) behind = carry;
                 if (r < cs) {
                     const Map m = chunks[par][r][col];
-                    carry = lfma(m.P(), carry, m.b());
+                    carry = lapply(m.q(), carry, m.b());
                 }
             }
-            cb = lfma(mp, behind, cb);
+            cb = lapply(mp, behind, cb);
         } else {
             if (k > 0) carry = last[par][col];
             cb = carry;
 #pragma unroll
             for (int w = W - 1; w > 0; --w)
-                if (w > warp) cb = lfma(maps[w].P(), cb, backs[w]);
-            if (warp == 0 && run == 0) last[par ^ 1][col] = lfma(maps[0].P(), cb, wr);
+                if (w > warp) cb = lapply(maps[w].q(), cb, backs[w]);
+            if (warp == 0 && run == 0) last[par ^ 1][col] = lapply(maps[0].q(), cb, wr);
         }
-        cb = lfma(ap, cb, ab);  // behind this run
+        if (Q > 1) cb = lapply(ap, cb, ab);  // behind this run
         L sr = zero, sg = zero;
         auto rest = [&](auto whole) {  // whole: every row and channel of the run is there
             constexpr bool kWhole = decltype(whole)::value;
@@ -337,7 +339,7 @@ __global__ void __launch_bounds__(kGatedBwdThreads, 2) gated_scan_bwd_kernel(con
 #pragma unroll
         for (int w = 0; w < W; ++w) {
             const Map r = runs[0][w][col];
-            drate = ladd(drate, r.P());
+            drate = ladd(drate, r.q());
             dbias = ladd(dbias, r.b());
         }
     }
@@ -354,7 +356,7 @@ __global__ void __launch_bounds__(kGatedBwdThreads, 2) gated_scan_bwd_kernel(con
             drate = dbias = zero;
             for (int r = 0; r < cs; ++r) {
                 const Map m = chunks[0][r][col];
-                drate = ladd(drate, m.P());
+                drate = ladd(drate, m.q());
                 dbias = ladd(dbias, m.b());
             }
         }

@@ -569,3 +569,72 @@ def test_refusals():
     ws = torch.empty(8, dtype=torch.uint8, device=x.device)
     with pytest.raises(_lib.JambaSSMError):
         jamba_ssm_gated_scan_bwd(x, g, x.clone(), workspace=ws)
+
+
+_SLOW = (2.0 ** -24, 1e-6, 1e-5, 1e-4)  # u is half of it: from below a half step of 1 on
+
+
+@pytest.mark.parametrize("dtype,batch,seqlen,d", [
+    (F32, 1, 16384, 8), (BF, 1, 16384, 64), (BF, 2, 8192, 33), (F32, 230, 8192, 32),
+    (F32, 300, 4096, 32), (BF, 1, 16000, 1024)])
+def test_slow_channels_stay_at_their_input(dtype, batch, seqlen, d):
+    """A state equal to its input does not move, however little a row forgets.
+
+    A run's decay n = P - 1 and its b have relative errors of 2 roundings a row and 2 a
+    join: at most (32 + 2 * 19) 2^-24 each, so n c + b, which is 0, is within 2^-16 c of
+    the run's own decay, and a state within 2^-16 c of its input stays there: rounding
+    to nearest keeps a value that moves towards c on its side of it.  A decay that is
+    rounded row by row moves the state by up to 2^-25 c a row instead."""
+    dev = _dev()
+    c = torch.linspace(0.6, 1.9, d, device=dev).to(dtype)
+    x = c.expand(batch, seqlen, d).contiguous()
+    g = torch.zeros_like(x)
+    rate = torch.tensor(_SLOW, device=dev).repeat(-(-d // 4))[:d].contiguous()
+    h0 = c.float().expand(batch, d).contiguous()
+    z = torch.ones_like(x) if dtype == F32 else None
+    ckpt = jamba_ssm_gated_scan_ckpt(x)
+    out, hf = jamba_ssm_gated_scan(x, g, z=z, rate=rate, h0=h0, ckpt=ckpt)
+    off = ((hf - h0).abs() / h0).amax(0)
+    assert (off <= 2.0 ** -16).all(), off[:4]
+    at = ckpt.reshape(-1, d)[: seqlen // 64]
+    assert ((at - h0[0]).abs() <= 2.0 ** -16 * h0[0]).all()
+    # a row's own state has the row-by-row error of its run, 16 roundings of P and of b
+    gate = 1.0 if z is None else torch.sigmoid(torch.ones((), dtype=torch.float64, device=dev))
+    half = 2.0 ** -8 if dtype == BF else 2.0 ** -22  # fp32: three roundings of the gate
+    assert ((out.double() / gate - h0.double()[:, None]).abs()
+            <= (2.0 ** -16 + 2.0 ** -19 + half) * h0[:, None]).all()
+
+
+@pytest.mark.parametrize("dtype,batch,seqlen,d", [
+    (F32, 1, 16384, 8), (BF, 1, 16384, 64), (BF, 2, 8192, 33), (F32, 300, 8192, 32)])
+def test_slow_channels_forget_at_their_rate(dtype, batch, seqlen, d):
+    """Forwards without input, and the gradient of h0 without dout: (1 - u)^rows.
+
+    A run rounds the state once, by 2^-24 of it at most, and its decay, 70 roundings of
+    itself (above): rows / 8 2^-24 and 2^-17 (1 - (1 - u)^rows) in all."""
+    dev = _dev()
+    x = torch.zeros(batch, seqlen, d, dtype=dtype, device=dev)
+    rate = torch.tensor(_SLOW, device=dev).repeat(-(-d // 4))[:d].contiguous()
+    one = torch.ones(batch, d, device=dev)
+    ckpt = jamba_ssm_gated_scan_ckpt(x)
+    _, hf = jamba_ssm_gated_scan(x, x, rate=rate, h0=one, ckpt=ckpt)
+    grads = jamba_ssm_gated_scan_bwd(x, x, x, rate=rate, h0=one, dh_final=one, ckpt=ckpt)
+    want = (1 - rate.double() / 2) ** seqlen
+    bound = seqlen / 8 * 2.0 ** -24 + 2.0 ** -17
+    for got, what in ((hf, "h_final"), (grads["dh0"], "dh0")):
+        off = (got.double() - want).abs().amax(0)
+        assert (off <= bound).all(), (what, off[:4], bound)
+
+
+@pytest.mark.parametrize("seqlen", [1, 16, 63, 100, 120])
+def test_fast_channels_forget_exactly(seqlen):
+    """u = 1/2: every product is a power of two, and nothing of a state is left but that."""
+    dev = _dev()
+    x = torch.zeros(2, seqlen, 40, device=dev)
+    h0 = torch.linspace(1, 3e4, 40, device=dev).repeat(2, 1)
+    ckpt = jamba_ssm_gated_scan_ckpt(x)
+    out, hf = jamba_ssm_gated_scan(x, x, h0=h0, ckpt=ckpt)
+    grads = jamba_ssm_gated_scan_bwd(x, x, x, h0=h0, dh_final=h0, ckpt=ckpt)
+    want = h0 * 2.0 ** -seqlen
+    assert torch.equal(hf, want) and torch.equal(out[:, -1], want)
+    assert torch.equal(grads["dh0"], want)
