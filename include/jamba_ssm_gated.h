@@ -164,7 +164,8 @@ jamba_ssm_status jamba_ssm_gated_scan_bwd(const jamba_ssm_gated_scan_bwd_params 
  *   x, g, z, out [batch, d_inner] io_dtype, x / g / z with row strides as
  *              above, z may be NULL; out contiguous, overlapping no input.
  *   state      [batch, d_inner] fp32, or a [num_slots, d_inner] cache whose row
- *              state_indices[b] is request b's.  A negative index skips the
+ *              state_indices[b] is request b's, read as it is: a new request's
+ *              row has to be zero.  A negative index skips the
  *              request (its out row stays as it was); an index >= num_slots is
  *              skipped too and recorded as JAMBA_SSM_ERR_INVALID_ARG.  Indices
  *              of one call must be distinct.

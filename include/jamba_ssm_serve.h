@@ -119,7 +119,11 @@ jamba_ssm_status jamba_ssm_i8_proj(const jamba_ssm_i8_proj_params *p, void *stre
  *                  scans' state_indices).
  *   initial_indices [requests]: as state_indices, but -1 where ctx is 0 (the
  *                  gated scan's initial_indices: a new request starts from
- *                  zero).
+ *                  zero).  The calls without initial_indices -- jamba_ssm_scan,
+ *                  jamba_ssm_state_update, jamba_ssm_gated_state_update -- start
+ *                  from row state_indices[b] whatever an earlier request left
+ *                  there: for them a slot's row is zeroed when the request that
+ *                  held it ends, before the slot is in free_slots again.
  *   counts         [4]: tokens, blocks taken, state slots taken, largest n.
  * Rows of the per-token maps behind the last token hold -1, so a captured step
  * of max_tokens rows can run on fewer.

@@ -181,8 +181,10 @@ def jamba_ssm_gated_state_update(state, x, g, z=None, rate=None, bias=None, out=
     """One token for each request; `state` [batch, d_inner] fp32 is updated in
     place.  x, g, z [batch, d_inner] (rows may be strided).  With
     ``state_indices`` (int32 [batch]) `state` is a [num_slots, d_inner] cache and
-    request b updates row state_indices[b]; a negative index skips the request
-    (its out row is left as it was).  Returns out [batch, d_inner]."""
+    request b updates row state_indices[b], as it is: a new request's row holds
+    zeros, or it takes its first token through jamba_ssm_gated_scan with
+    initial_indices; a negative index skips the request (its out row is left as
+    it was).  Returns out [batch, d_inner]."""
     dev = cuda_device(x, "x", "jamba_ssm_gated_state_update")
     if x.dtype not in IO:
         raise TypeError(f"x must be bfloat16 or float32, got {x.dtype}")

@@ -114,7 +114,10 @@ def jamba_ssm_batch_maps(new_lens, block_tables, free_blocks, request_slots, fre
     Returns a dict: cu_seqlens [requests + 1], positions, token_request
     [max_tokens], slot_map int64 [max_tokens], block_tables, request_slots,
     state_indices, initial_indices [requests], counts [4] = tokens, blocks
-    taken, slots taken, longest request.  What does not fit (tokens past
+    taken, slots taken, longest request.  initial_indices lets the gated scan
+    start a new request from zero; jamba_ssm_scan and the one-token updates read
+    the row of its slot: for them zero the row (``cache[slot] = 0``) when the
+    request that held it ends, before the slot is in free_slots again.  What does not fit (tokens past
     max_tokens, no free block or slot, a request longer than its table) is
     recorded in the status word (jamba_ssm_serve_get_status)."""
     dev = cuda_device(new_lens, "new_lens", "jamba_ssm_batch_maps")

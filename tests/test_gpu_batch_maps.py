@@ -310,3 +310,68 @@ def test_status_without_a_device_index():
     for device in (None, "cuda", torch.device("cuda"), 0):
         assert jamba_ssm_serve_get_status(device=device) == 0
         assert jamba_ssm_gated_get_status(device=device) == 0
+
+
+def test_recycled_slots_and_the_selective_scan():
+    """Two steps of a continuous batch through jamba_ssm_scan, then a decode step.  A
+    request of the second step gets the slot of one that ended: its row was zeroed
+    then, so every request's outputs are those of its tokens alone, from zero.  Left as
+    it was, the row would be the new request's initial state."""
+    from selective_state_space_26_b200 import (jamba_ssm_get_status, jamba_ssm_scan,
+                                               jamba_ssm_state_update, synth)
+    from tests.parity import assert_out
+    from tests.test_gpu_serving import _oracle_seq
+    _i32([0])
+    d, n, bf = 128, 16, torch.bfloat16
+    # rows: requests 0 to 3; request 3 comes in the second step
+    inp = synth.scan_inputs(4, 90, d, n, bf, seed=21, device="cuda", A_kind="random")
+    cache = torch.zeros(3, d, n, device="cuda")
+    args = dict(D=inp.D, delta_bias=inp.delta_bias)
+    done, free_s = [0] * 4, [2, 0, 1]
+    table = torch.full((3, 8), -1, dtype=torch.int32, device="cuda")
+    slots = torch.full((3,), -1, dtype=torch.int32, device="cuda")
+    outs = [[] for _ in range(4)]
+
+    def step(who, lens):
+        nonlocal free_s
+        cat = lambda t: torch.cat([t[r, done[r]:done[r] + k] for r, k in zip(who, lens)])  # noqa: E731
+        maps = jamba_ssm_batch_maps(_i32(lens), table, _i32(list(range(40))), slots, _i32(free_s),
+                                    ctx_lens=_i32([done[r] for r in who]), block_size=16,
+                                    max_tokens=sum(lens))
+        free_s = free_s[maps["counts"].tolist()[2]:]
+        out, _ = jamba_ssm_scan(cat(inp.x), cat(inp.delta), cat(inp.z), cat(inp.B), cat(inp.C),
+                                inp.A, **args, h0=cache, h_final=cache,
+                                cu_seqlens=maps["cu_seqlens"],
+                                state_indices=maps["state_indices"])
+        for r, k, o in zip(who, lens, out.split(lens)):
+            outs[r].append(o)
+            done[r] += k
+        return maps
+
+    step([0, 1, 2], [40, 17, 64])
+    ended = int(slots[1])
+    left = cache[ended].clone()
+    assert left.abs().max() > 0
+    cache[ended] = 0
+    free_s.append(ended)
+    table[1], slots[1] = -1, -1
+    maps = step([0, 3, 2], [1, 50, 20])  # request 3 in the place of 1, with its slot
+    assert maps["state_indices"].tolist()[1] == ended and maps["initial_indices"].tolist()[1] == -1
+    maps = jamba_ssm_batch_maps(_i32([1, 1, 1]), table, _i32([]), slots, _i32([]),
+                                ctx_lens=_i32([done[0], done[3], done[2]]), block_size=128,
+                                max_tokens=3)
+    row = lambda t: torch.stack([t[r, done[r]] for r in (0, 3, 2)])  # noqa: E731
+    y = jamba_ssm_state_update(cache, row(inp.x), row(inp.delta), row(inp.z), row(inp.B),
+                               row(inp.C), inp.A, **args, state_indices=maps["state_indices"])
+    for i, r in enumerate((0, 3, 2)):
+        outs[r].append(y[i:i + 1])
+        done[r] += 1
+    for r in range(4):
+        ref, _ = _oracle_seq(inp, r, done[r])
+        assert_out(torch.cat(outs[r]), ref, bf, f"request {r}")
+    # the row left as it was
+    stale = jamba_ssm_scan(inp.x[3, :50], inp.delta[3, :50], inp.z[3, :50], inp.B[3, :50],
+                           inp.C[3, :50], inp.A, **args, h0=left[None], cu_seqlens=_i32([0, 50]),
+                           h_final=left.clone()[None], state_indices=_i32([0]))[0]
+    assert not torch.equal(stale, outs[3][0])
+    assert jamba_ssm_get_status() == 0 and jamba_ssm_serve_get_status() == 0
