@@ -3,10 +3,10 @@
  * (libjamba_ssm_gated.so, sm_100a): the scan over whole sequences, its
  * backward pass and the one-token update.
  *
- * The operation.  It is the selective recurrence of the "Mamba 레이어" section
- * ("Jamba: A Hybrid Transformer-Mamba Language Model", obsidian-dorae222
- * notes), h_t = Abar_t h_{t-1} + Bbar_t x_t, with one state per channel whose
- * decay and input weight come from one gate of the token and add up to one:
+ * The operation.  A recurrence of its own beside jamba_ssm.h's selective one
+ * (h_t = Abar_t h_{t-1} + Bbar_t x_t, which is that of Jamba's layers): one state
+ * per channel, whose decay and input weight come from one gate of the token and
+ * add up to one:
  *     u_t   = rate[d] * sigmoid(g_t + bias[d])           (update rate)
  *     h_t   = h_{t-1} + u_t (x_t - h_{t-1})              = (1 - u_t) h_{t-1} + u_t x_t
  *     out_t = h_t * silu(z_t),  silu(z) = z / (1 + e^-z)   (no z: out_t = h_t)
@@ -48,7 +48,10 @@ extern "C" {
  * Sizes: batch >= 0, seqlen >= 0, d_inner in [1, 2^20]; any width, no
  * alignment beyond the element's (even widths, strides and 2-element aligned
  * pointers take the kernels whose lanes hold two channels).  At most 2^30
- * token rows, 2^24 sequences.
+ * token rows, 2^24 sequences, and 2^31 - 1 sequences times ceil(d_inner / 32)
+ * (JAMBA_SSM_ERR_UNSUPPORTED beyond).  Packed sequences are cut by their mean
+ * length: one that is much longer than three times the mean takes longer than
+ * it would in a call of its own.
  * Pointers (device):
  *   x, g, z    [batch, seqlen, d_inner] io_dtype; z may be NULL.  Row r of x
  *              starts x_stride elements after row r - 1 (batches follow one

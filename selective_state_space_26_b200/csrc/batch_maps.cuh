@@ -10,8 +10,8 @@
 // sums in shared memory (the lengths come from L2) and then map 1024 tokens: a
 // second launch, or a wait for one CTA's sums, would cost more than the few
 // thousand additions.  It is bound by latency: a load of the lengths, two block
-// scans, a search and a store (256 requests of one token: 5.7 us; 1000 requests,
-// 131072 tokens: 6.7 us, of which the 2.1 MB of maps would take 0.3).  More
+// scans, a search and a store (256 requests of one token: 5.5 us; 1000 requests,
+// 131072 tokens: 6.4 us, of which the 2.1 MB of maps would take 0.3).  More
 // requests take two launches, the second searching the first's cu_seqlens.
 #pragma once
 

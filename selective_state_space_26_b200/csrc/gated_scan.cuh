@@ -328,7 +328,7 @@ template <typename T, int VEC, int S, int Q, int CP> struct GatedFeed {
 // rows lie together, the runs apart so that their lanes' words fall into different
 // banks.  Bytes of neighbouring rows and channels come along unused; nothing before
 // the array is read, and behind it a copy is cut short.  A row of 64 bytes takes 5 of
-// an instruction's lanes in place of 16: 13 x 4096 x 1026 bf16 with z 135 us for 184.
+// an instruction's lanes in place of 16: 13 x 4096 x 1026 bf16 with z 125 us for 184.
 constexpr int kCpShifted = 0;
 template <typename T, int VEC, int S, int Q> struct GatedShiftedFeed {
     static constexpr int kRow = 128 / Q;              // bytes of a row
@@ -435,13 +435,15 @@ __device__ __forceinline__ Lane2 lshfl_down(Lane2 a, int by) {
 // barrier per round.
 //
 // What bounds it: HBM in fp32 (4096 x 4096 with z: 44 us, 6.1 TB/s); in bf16,
-// where an element is half the bytes for the same arithmetic, the issue slots
-// and the special-function pipe come close (13 x 4096 x 2048: 158 us, 5.5 TB/s;
-// 8192 channels by 4096 rows, with 256 tiles on 148 SMs: 57 us, 4.7 TB/s).  The
-// steps there, us at 13 x 4096 x 2048: runs of 8 rows and 8 warps 174, without
-// the copies 143, without the sigmoids too 107; runs of 16 and 4 warps, which
-// halve the exchange's share of a row, 158.  A reciprocal for each sigmoid, and
-// three or four stages instead of two, were slower or no faster.
+// where an element is half the bytes for the same arithmetic, a round's latency at
+// the 16 warps an SM that 128 registers leave: 13 x 4096 x 2048 takes 161 to 168 us
+// (5.2 to 5.4 TB/s), and in the like 8 x 2048 x 4096 the issue slots and the
+// special-function pipe are half used; 8192 channels by 4096 rows, with 256 tiles on
+// 148 SMs, 59 us (4.6 TB/s).  The steps there, us at 13 x 4096 x 2048 before the maps
+// held P - 1: runs of 8 rows and 8 warps 174, without the copies 143, without the
+// sigmoids too 107; runs of 16 and 4 warps, which halve the exchange's share of a row,
+// 158.  A reciprocal for each sigmoid, and three or four stages instead of two, were
+// slower or no faster.
 constexpr int kGatedMaxCluster = 8;
 constexpr int kGatedRun = 16;
 

@@ -18,12 +18,13 @@
 // the sequences, each in a fixed order.
 //
 // It reads x, g, z and dout once and writes dx, dg and dz once: with the
-// forward and its checkpoints, 8 x 2048 x 4096 bf16 take 292 us (5.05 TB/s, 77%
-// of a plain copy), 2 x 4096 x 4096, whose 256 CTAs leave an SM two at most, 166.
-// What bounds it is the issue slots, about 120 a row and warp.  Runs of 16 rows
-// on 4 warps (381 and 209 us) spread the exchange over more rows but leave half
-// the warps to hide each other's latency; testing a row for the run's end inside
-// the loops costs 328 and 179.
+// forward and its checkpoints, 8 x 2048 x 4096 bf16 take 302 us (4.9 TB/s, 75%
+// of a plain copy), 2 x 4096 x 4096, whose 256 CTAs leave an SM two at most, 169.
+// What bounds it is latency at the 16 warps an SM that 128 registers leave: a row
+// and warp takes 123 instructions, and 56% of the issue slots are used.  Before the
+// maps held P - 1 (292 and 166 us): runs of 16 rows on 4 warps (381 and 209) spread
+// the exchange over more rows but leave half the warps to hide each other's latency;
+// testing a row for the run's end inside the loops costs 328 and 179.
 #pragma once
 
 #include "gated_scan.cuh"

@@ -4,9 +4,10 @@
 //
 // A thread takes V neighbouring channels of one request: 8 bf16 or 4 fp32 (one
 // 16-byte load each of x, g and z, two of the state for bf16) where rows begin
-// at 16-byte boundaries, else 1.  Bound by HBM for many requests (every byte
-// moves once: 256 x 8192 bf16 in 5.5 us, 6.1 TB/s) and by the launch for few
-// (5 x 1027 fp32: 1.9 us), so it begins while the work before it ends.
+// at 16-byte boundaries, else 1.  Every byte moves once: 256 x 8192 bf16 from HBM
+// take 7.6 us (4.4 TB/s, start and tail of one wave among it), 5.5 where L2 still
+// holds a part; few requests are bound by the launch (5 x 1027 fp32: 1.6 us), so it
+// begins while the work before it ends.
 #pragma once
 
 #include "device_utils.cuh"

@@ -179,9 +179,9 @@ struct I8Wait {
 // so a 128-byte block of K costs an SM 32 KB for 256 x 256 x 128 products of
 // the pair -- a third less from L2 than a CTA of its own with 128 x 256.  Six
 // stages; two accumulators of 256 TMEM columns, so a tile's outputs are written
-// while the next tile's products run.  4096 x 4096 x 16384: 158 us alone, the
-// tensor pipe 83% active; 178 to 205 back to back, where the power limit lowers
-// the clock.  What the outputs cost shows at K 4096 and below: 205 us with 4 warps
+// while the next tile's products run.  4096 x 4096 x 16384: 158 to 175 us alone, by
+// the clock, the tensor pipe 83% active; 178 to 205 back to back, where the power
+// limit lowers the clock.  What the outputs cost shows at K 4096 and below: 205 us with 4 warps
 // that wrote one bf16 channel at a time, 181 with two channels a word, 178 with 8.
 struct I8PairCfg {
     static constexpr int kTile = 256;               // channels and tokens of a pair's tile
@@ -350,7 +350,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(I8PairCfg::kThreads,
 // tile's K until the device is full, every CTA with up to 200 KB of the weight
 // on its way.  The cluster then adds its partial sums: each CTA sends every
 // other one the columns that it finishes, through distributed shared memory.
-// 8 tokens, K 8192, 4096 channels: 9.4 us (3.6 TB/s of weight), 4 CTAs to a tile.
+// 8 tokens, K 8192, 4096 channels, 4 CTAs to a tile: 10.9 us with the weight from HBM
+// (3.1 TB/s of it), 9.4 where L2 still holds a part; K 4096, 16384 channels 15.4 (4.4).
 template <int NT> struct I8SplitCfg {
     static constexpr int kM = 128;
     static constexpr int kA = kM * 128, kB = NT * 128;

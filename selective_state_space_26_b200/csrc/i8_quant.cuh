@@ -120,7 +120,7 @@ template <> struct I8Eight<float> {
 // LANES threads take a row, eight elements at a time; the first kKept of a
 // thread's eights stay in registers between the two passes (every row of up to
 // 8 * LANES * kKept elements is read once), the others are read again, from L2.
-// VECTOR: rows begin at 16-byte boundaries.  4096 x 4096 bf16: 12.6 us, 4.0 TB/s;
+// VECTOR: rows begin at 16-byte boundaries.  4096 x 4096 bf16: 13.3 us, 3.8 TB/s;
 // bound by the arithmetic, about 6 instructions an element (with floor and
 // convert instructions in their place 19 us).
 constexpr int kQuantThreads = 256, kQuantKept = 4;

@@ -83,7 +83,8 @@ struct Cut {
 
 // Of a pass over sequences of tiles(q) channel tiles each.  A CTA of q = 1 reads 128 bytes of a row and takes 64 rows a round;
 // q = 2 and 4 halve and quarter the width for two and four times the rows.
-// Measured on 148 SMs (bf16 with z, us):
+// Measured on 148 SMs (bf16 with z, us; before the maps held P - 1, which takes
+// about 3% more on every side):
 //   8192 channels, 4096 rows:  q 1 89, q 2 59, q 4 72, q 2 in clusters of 2 68;
 //   2048 channels, 65536 rows: q 2 in clusters of 8 264, of 4 378, q 4 of 4 303;
 //   512 channels, 8192 rows:   q 4 in clusters of 8 17, q 2 of 8 26, q 1 of 8 37;
@@ -97,6 +98,10 @@ struct Cut {
 // run on alone, so q goes up until its rounds take no longer than moving all
 // the bytes (9 sequences, 3001 rows of 1000 fp32 channels, both passes: q 1 112,
 // q 2 66, q 4 52; 33 sequences, 16384 rows of 4096: q 1 94, q 2 113, q 4 160).
+// The host does not know the lengths.  Where one is far longer than that, it does
+// run on alone: 8192 rows and 255 of one row, 4096 channels, 219 us, 357 with the
+// long one last (more sequences than a CTA has threads keep their order), for 70 of
+// the long one by itself.
 struct Pass {
     int per_sm, per_sm4;  // CTAs that fit an SM, and of q = 4
     int halves;           // half CTAs to an SM from which q = 2 takes no cluster
